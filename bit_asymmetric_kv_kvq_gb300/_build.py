@@ -24,7 +24,7 @@ DEBUG_OBJDIR = os.path.join(LIBDIR, "obj_debug")
 DEBUG_FLAGS = ("-DKVQ_DEBUG_CHECKS",)
 
 SOURCES = ["kvq_api.cpp", "kvq_quant.cu", "kvq_decode.cu", "kvq_decode_lut.cu", "kvq_decode_mma.cu", "kvq_noalloc.cu",
-           "kvq_ablation.cu"]
+           "kvq_ablation.cu", "kvq_rope.cu", "kvq_copy.cu", "kvq_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

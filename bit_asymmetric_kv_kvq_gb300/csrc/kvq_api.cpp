@@ -337,6 +337,159 @@ cudaError_t copy_to_sink(kvq_cache* c, const void* k, const void* v, int64_t src
   return e;
 }
 
+// Quantize n_pages * R tokens of a [units][src_tokens][D] pair of buffers, from token src_tok0 on, into
+// the pages from page0 on.
+cudaError_t quantize_from(kvq_cache* c, const void* k, const void* v, int64_t src_tokens, int64_t src_tok0,
+                          int64_t page0, int64_t n_pages, cudaStream_t s) {
+  const int R = c->cfg.residual, D = c->cfg.head_dim;
+  // one launch per at most 65535 pages in grid.x
+  for (int64_t p0 = 0; p0 < n_pages; p0 += 65535) {
+    const int64_t np = n_pages - p0 < 65535 ? n_pages - p0 : 65535;
+    kvq::QuantizeParams qp{};
+    qp.k_src = static_cast<const uint16_t*>(k);
+    qp.v_src = static_cast<const uint16_t*>(v);
+    qp.src_unit_stride = src_tokens * D;
+    qp.src_tok0 = src_tok0 + p0 * R;
+    qp.pages = c->pages;
+    qp.unit_page_stride = c->unit_page_stride;
+    qp.page0 = page0 + p0;
+    qp.n_units = (int32_t)c->n_units;
+    qp.Hkv = c->cfg.num_kv_heads;
+    qp.D = D;
+    qp.G = c->cfg.group_size;
+    qp.R = R;
+    qp.nsp = c->cfg.k_sparse;
+    qp.lay = c->lay;
+    qp.err = c->err;
+    qp.src_elems = c->n_units * src_tokens * D;
+    qp.pages_bytes = c->n_units * c->unit_page_stride;
+    set_codebook(c, &qp);
+    const cudaError_t e = kvq::launch_quantize(qp, c->cfg.k_bits, c->cfg.v_bits, (int)np, s);
+    if (e != cudaSuccess) return e;
+    c->launches++;
+  }
+  return cudaSuccess;
+}
+
+// Copy n_tok tokens, from token src_tok0 of a [units][src_tokens][D] pair of buffers, behind the
+// window's tokens (the sink is full: n_s = S).
+cudaError_t copy_to_window(kvq_cache* c, const void* k, const void* v, int64_t src_tokens, int64_t src_tok0,
+                           int32_t n_tok, cudaStream_t s) {
+  const int D = c->cfg.head_dim;
+  kvq::CopyTokensParams cp{};
+  cp.k_src = static_cast<const uint16_t*>(k);
+  cp.v_src = static_cast<const uint16_t*>(v);
+  cp.src_unit_stride = src_tokens * D;
+  cp.src_tok0 = src_tok0;
+  cp.k_dst = c->wk;
+  cp.v_dst = c->wv;
+  cp.dst_unit_stride = rows_per_unit(c) * D;
+  cp.dst_tok0 = c->n_s + c->n_r;
+  cp.n_tok = n_tok;
+  cp.n_units = (int32_t)c->n_units;
+  cp.D = D;
+  const cudaError_t e = kvq::launch_copy_tokens(cp, s);
+  if (e == cudaSuccess) {
+    c->launches++;
+    c->n_r += n_tok;
+  }
+  return e;
+}
+
+// Append tokens 0 .. n of a [units][src_tokens][D] pair of buffers: the state machine of kvq_append
+// run over whole stretches.  Every token goes where n single appends would put it: a stretch of
+// whole pages is quantized straight from the source only when the window is empty (after a flush, or
+// on an empty cache) and at least one token follows it for the window to hold.
+cudaError_t append_tokens(kvq_cache* c, const void* k, const void* v, int64_t n, int64_t src_tokens, cudaStream_t s) {
+  const int R = c->cfg.residual;
+  int64_t at = 0;
+  cudaError_t e = cudaSuccess;
+  if (c->n_s < c->cfg.sink_tokens) {
+    const int64_t room = c->cfg.sink_tokens - c->n_s;
+    const int64_t ns = n < room ? n : room;
+    e = copy_to_sink(c, k, v, src_tokens, 0, (int32_t)ns, s);
+    at = ns;
+  }
+  while (e == cudaSuccess && at < n) {
+    if (c->n_r == R) {
+      e = flush_window(c, s);
+      if (e != cudaSuccess) break;
+    }
+    if (c->n_r == 0 && n - at > R) {
+      const int64_t np = (n - at - 1) / R;
+      e = quantize_from(c, k, v, src_tokens, at, c->Tq / R, np, s);
+      if (e != cudaSuccess) break;
+      c->Tq += np * R;
+      at += np * R;
+    }
+    const int64_t room = R - c->n_r;
+    const int64_t take = n - at < room ? n - at : room;
+    e = copy_to_window(c, k, v, src_tokens, at, (int32_t)take, s);
+    at += take;
+  }
+  if (e == cudaSuccess) {
+    c->T += n;
+    c->prefilled = true;
+  }
+  return e;
+}
+
+kvq_status launch_chunk_for(kvq_cache* c, const void* k, const void* v, const void* q, int64_t n, void* out,
+                            void* workspace, cudaStream_t s) {
+  kvq::ChunkParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_new = static_cast<const uint16_t*>(k);
+  p.v_new = static_cast<const uint16_t*>(v);
+  p.out = static_cast<uint16_t*>(out);
+  p.pages = c->pages;
+  p.unit_page_stride = c->unit_page_stride;
+  p.wk = c->wk;
+  p.wv = c->wv;
+  p.win_unit_stride = rows_per_unit(c) * c->cfg.head_dim;
+  p.n_units = c->n_units;
+  p.n_pages = c->Tq / c->cfg.residual;
+  p.n = n;
+  p.Tq = c->Tq;
+  p.n_s = c->n_s;
+  p.n_w = c->n_s + c->n_r;
+  p.Hkv = c->cfg.num_kv_heads;
+  p.Hq = c->cfg.num_q_heads;
+  const int hg = c->cfg.num_q_heads / c->cfg.num_kv_heads;
+  p.log2hg = hg == 4 ? 2 : hg == 2 ? 1 : 0;
+  p.G = c->cfg.group_size;
+  p.R = c->cfg.residual;
+  p.nsp = c->cfg.k_sparse;
+  p.bk = c->cfg.k_bits;
+  p.bv = c->cfg.v_bits;
+  p.lay = c->lay;
+  p.scale_log2 = c->cfg.softmax_scale * 1.4426950408889634f;
+  p.rope_turns = c->rope_turns;
+  p.err = c->err;
+  if (c->cfg.codebook) {
+    p.lut = 1;
+    std::memcpy(p.k_lev, c->k_lev, sizeof(p.k_lev));
+    std::memcpy(p.v_lev, c->v_lev, sizeof(p.v_lev));
+  }
+  int launches = 0;
+  const cudaError_t e = kvq::launch_chunk(p, c->cfg.rope != 0, c->sm_count, workspace, &launches, s);
+  c->launches += launches;
+  return e == cudaSuccess ? KVQ_OK : fail_cuda(c);
+}
+
+// Argument checks that kvq_chunk_attention and kvq_chunk_step share.
+kvq_status check_chunk(const kvq_cache* c, const void* k, const void* v, const void* q, int64_t n, const void* out,
+                       const void* workspace, int64_t workspace_bytes) {
+  if (!c || !k || !v || !q || !out || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (c->broken) return KVQ_ERR_CUDA;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return KVQ_ERR_INVALID_ARG;
+  if (n < 1 || n >= ((int64_t)1 << 31) - c->T) return KVQ_ERR_INVALID_ARG;
+  const int hg = c->cfg.num_q_heads / c->cfg.num_kv_heads;
+  if (workspace_bytes < kvq::chunk_workspace_bytes(n, hg, c->sm_count)) return KVQ_ERR_INVALID_ARG;
+  if (c->cfg.codebook && !c->lut_set) return KVQ_ERR_STATE;
+  return KVQ_OK;
+}
+
 // Decode attention over the cache's current state.  k_new/v_new are null, or hold the window's
 // newest token (slot n_r - 1), which the kernel then reads from there and stores into the window.
 kvq_status launch_decode_for(kvq_cache* c, const void* q, void* out, const void* k_new, const void* v_new,
@@ -639,31 +792,7 @@ kvq_status kvq_prefill_quantize(kvq_cache* c, const void* k, const void* v, int6
   if (ns > 0 && copy_to_sink(c, k, v, n_tokens, 0, (int32_t)ns, s) != cudaSuccess) return fail_cuda(c);
   const int64_t Tq = quantized_tokens(n_tokens - ns, R);
   const int64_t n_pages = Tq / R;
-  // one launch per at most 65535 pages in grid.x
-  for (int64_t p0 = 0; p0 < n_pages; p0 += 65535) {
-    const int64_t np = n_pages - p0 < 65535 ? n_pages - p0 : 65535;
-    kvq::QuantizeParams qp{};
-    qp.k_src = static_cast<const uint16_t*>(k);
-    qp.v_src = static_cast<const uint16_t*>(v);
-    qp.src_unit_stride = n_tokens * D;
-    qp.src_tok0 = ns + p0 * R;
-    qp.pages = c->pages;
-    qp.unit_page_stride = c->unit_page_stride;
-    qp.page0 = p0;
-    qp.n_units = (int32_t)c->n_units;
-    qp.Hkv = c->cfg.num_kv_heads;
-    qp.D = D;
-    qp.G = c->cfg.group_size;
-    qp.R = R;
-    qp.nsp = c->cfg.k_sparse;
-    qp.lay = c->lay;
-    qp.err = c->err;
-    qp.src_elems = c->n_units * n_tokens * D;
-    qp.pages_bytes = c->n_units * c->unit_page_stride;
-    set_codebook(c, &qp);
-    if (kvq::launch_quantize(qp, c->cfg.k_bits, c->cfg.v_bits, (int)np, s) != cudaSuccess) return fail_cuda(c);
-    c->launches++;
-  }
+  if (quantize_from(c, k, v, n_tokens, ns, 0, n_pages, s) != cudaSuccess) return fail_cuda(c);
   kvq::CopyTokensParams cp{};
   cp.k_src = static_cast<const uint16_t*>(k);
   cp.v_src = static_cast<const uint16_t*>(v);
@@ -721,6 +850,111 @@ kvq_status kvq_append(kvq_cache* c, const void* k, const void* v, void* stream) 
   c->n_r += 1;
   c->T += 1;
   c->prefilled = true;
+  return KVQ_OK;
+}
+
+kvq_status kvq_append_chunk(kvq_cache* c, const void* k, const void* v, int64_t n_tokens, int64_t src_tokens,
+                            void* stream) {
+  if (!c || !k || !v) return KVQ_ERR_INVALID_ARG;
+  if (c->broken) return KVQ_ERR_CUDA;
+  if (!aligned16(k) || !aligned16(v)) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens < 1 || src_tokens < n_tokens || src_tokens > ((int64_t)1 << 40)) return KVQ_ERR_INVALID_ARG;
+  if (c->cfg.codebook && !c->lut_set) return KVQ_ERR_STATE;
+  if (n_tokens > c->cfg.max_tokens - c->T) return KVQ_ERR_CAPACITY;
+  DeviceGuard g(c->device);
+  if (!g.ok) return fail_cuda(c);
+  return append_tokens(c, k, v, n_tokens, src_tokens, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
+                                                                                                       : fail_cuda(c);
+}
+
+kvq_status kvq_chunk_workspace(const kvq_cache* c, int64_t n_tokens, int64_t* bytes) {
+  if (!c || !bytes || n_tokens < 1) return KVQ_ERR_INVALID_ARG;
+  *bytes = kvq::chunk_workspace_bytes(n_tokens, c->cfg.num_q_heads / c->cfg.num_kv_heads, c->sm_count);
+  return KVQ_OK;
+}
+
+kvq_status kvq_chunk_attention(kvq_cache* c, const void* k, const void* v, const void* q, int64_t n_tokens, void* out,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  const kvq_status st = check_chunk(c, k, v, q, n_tokens, out, workspace, workspace_bytes);
+  if (st != KVQ_OK) return st;
+  DeviceGuard g(c->device);
+  if (!g.ok) return fail_cuda(c);
+  return launch_chunk_for(c, k, v, q, n_tokens, out, workspace, static_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_chunk_step(kvq_cache* c, const void* k, const void* v, const void* q, int64_t n_tokens, void* out,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+  const kvq_status st = check_chunk(c, k, v, q, n_tokens, out, workspace, workspace_bytes);
+  if (st != KVQ_OK) return st;
+  if (n_tokens > c->cfg.max_tokens - c->T) return KVQ_ERR_CAPACITY;
+  DeviceGuard g(c->device);
+  if (!g.ok) return fail_cuda(c);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const kvq_status at = launch_chunk_for(c, k, v, q, n_tokens, out, workspace, s);
+  if (at != KVQ_OK) return at;
+  return append_tokens(c, k, v, n_tokens, n_tokens, s) == cudaSuccess ? KVQ_OK : fail_cuda(c);
+}
+
+kvq_status kvq_copy_sequences(kvq_cache* dst, kvq_cache* src, const int32_t* index, void* stream) {
+  if (!dst || !src || !index) return KVQ_ERR_INVALID_ARG;
+  if (dst->broken || src->broken) return KVQ_ERR_CUDA;
+  if (reinterpret_cast<uintptr_t>(index) % 4) return KVQ_ERR_INVALID_ARG;
+  kvq_config a = dst->cfg, b = src->cfg;
+  if (a.num_kv_heads != b.num_kv_heads || a.num_q_heads != b.num_q_heads || a.head_dim != b.head_dim ||
+      a.k_bits != b.k_bits || a.v_bits != b.v_bits || a.group_size != b.group_size || a.residual != b.residual ||
+      a.k_sparse != b.k_sparse || a.rope != b.rope || (a.rope && a.rope_base != b.rope_base) ||
+      a.softmax_scale != b.softmax_scale || a.sink_tokens != b.sink_tokens || a.codebook != b.codebook ||
+      dst->device != src->device)
+    return KVQ_ERR_INVALID_ARG;
+  if (a.codebook) {
+    if (!dst->lut_set || !src->lut_set) return KVQ_ERR_STATE;
+    if (std::memcmp(dst->k_lev, src->k_lev, sizeof(src->k_lev)) || std::memcmp(dst->v_lev, src->v_lev, sizeof(src->v_lev)))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  if (src->T > a.max_tokens) return KVQ_ERR_CAPACITY;
+  const bool in_place = dst == src;
+  if (in_place && a.batch > kvq::copy_sequences_max_in_place()) return KVQ_ERR_UNSUPPORTED;
+  if (src->T > 0) {
+    DeviceGuard g(dst->device);
+    if (!g.ok) return fail_cuda(dst);
+    const int64_t row_bytes = rows_per_unit(src) * a.head_dim * 2;  // both caches: sink_tokens and R agree
+    const int64_t rows = (int64_t)(src->n_s + src->n_r) * a.head_dim * 2;
+    kvq::CopySequencesParams p{};
+    auto run = [](const void* s, void* d, int64_t ss, int64_t ds, int64_t bytes) {
+      return kvq::CopyRun{static_cast<const uint8_t*>(s), static_cast<uint8_t*>(d), ss, ds, bytes / 16};
+    };
+    p.run[0] = run(src->pages, dst->pages, src->unit_page_stride, dst->unit_page_stride,
+                   src->Tq / a.residual * (int64_t)src->lay.bytes);
+    p.run[1] = run(src->wk, dst->wk, row_bytes, row_bytes, rows);
+    p.run[2] = run(src->wv, dst->wv, row_bytes, row_bytes, rows);
+    p.index = index;
+    p.n_src = b.batch;
+    p.n_dst = a.batch;
+    p.Hkv = a.num_kv_heads;
+    p.in_place = in_place ? 1 : 0;
+    p.err = dst->err;
+    if (kvq::launch_copy_sequences(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return fail_cuda(dst);
+    dst->launches++;
+  }
+  if (!in_place) {
+    dst->T = src->T;
+    dst->Tq = src->Tq;
+    dst->n_r = src->n_r;
+    dst->n_s = src->n_s;
+    dst->prefilled = src->prefilled;
+  }
+  return KVQ_OK;
+}
+
+kvq_status kvq_buffers(const kvq_cache* c, kvq_device_view* view) {
+  if (!c || !view) return KVQ_ERR_INVALID_ARG;
+  view->pages = c->pages;
+  view->wk = c->wk;
+  view->wv = c->wv;
+  view->pages_per_unit = c->n_pages_cap;
+  view->page_bytes = c->lay.bytes;
+  view->rows_per_unit = rows_per_unit(c);
+  view->n_units = c->n_units;
   return KVQ_OK;
 }
 

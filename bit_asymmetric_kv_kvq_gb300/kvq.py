@@ -13,6 +13,7 @@ Two layers:
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -60,6 +61,25 @@ class kvq_page_info(ctypes.Structure):
                [("tokens_per_page", ctypes.c_int32), ("fragment_order", ctypes.c_int32)]
 
 
+class kvq_device_view(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "wk", "wv")] + \
+               [(n, ctypes.c_int64) for n in ("pages_per_unit", "page_bytes", "rows_per_unit", "n_units")]
+
+
+class kvq_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("attention_factor", ctypes.c_double),
+                ("original_context", ctypes.c_int64)]
+
+
+class kvq_rope_part(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("x_batch_stride", "x_token_stride", "x_head_stride", "out_batch_stride",
+                                              "out_token_stride", "out_head_stride")] + \
+               [("num_heads", ctypes.c_int32), ("rotate", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _lock = threading.Lock()
 _lib = None
@@ -91,6 +111,14 @@ SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kvq_version": (ctypes.c_int32, []),
     "kvq_page_layout": (ctypes.c_int, [ctypes.POINTER(kvq_config), ctypes.POINTER(kvq_page_info)]),
+    "kvq_append_chunk": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int64, _P]),
+    "kvq_chunk_attention": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P]),
+    "kvq_chunk_step": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P]),
+    "kvq_chunk_workspace": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
+    "kvq_copy_sequences": (ctypes.c_int, [_P, _P, _P, _P]),
+    "kvq_buffers": (ctypes.c_int, [_P, ctypes.POINTER(kvq_device_view)]),
+    "kvq_rope": (ctypes.c_int, [ctypes.POINTER(kvq_rope_config), ctypes.POINTER(kvq_rope_part), ctypes.c_int32,
+                                ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _P, ctypes.c_int64, _P]),
     "kvq_axis_quantize": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]),
     "kvq_axis_dequantize": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
@@ -287,6 +315,37 @@ def kvq_set_codebooks(handle, k_levels, v_levels) -> None:
     _check(lib().kvq_set_codebooks(handle, k.ctypes.data, v.ctypes.data), "kvq_set_codebooks")
 
 
+def kvq_append_chunk(handle, k, v, n_tokens: int, src_tokens: int, stream=None) -> None:
+    _check(lib().kvq_append_chunk(handle, _ptr(k), _ptr(v), n_tokens, src_tokens, _stream(stream)), "kvq_append_chunk")
+
+
+def kvq_chunk_workspace(handle, n_tokens: int) -> int:
+    """Bytes of workspace a chunk of up to n_tokens tokens needs."""
+    n = ctypes.c_int64()
+    _check(lib().kvq_chunk_workspace(handle, n_tokens, ctypes.byref(n)), "kvq_chunk_workspace")
+    return n.value
+
+
+def kvq_chunk_attention(handle, k, v, q, n_tokens: int, out, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().kvq_chunk_attention(handle, _ptr(k), _ptr(v), _ptr(q), n_tokens, _ptr(out), _ptr(workspace),
+                                     workspace_bytes, _stream(stream)), "kvq_chunk_attention")
+
+
+def kvq_chunk_step(handle, k, v, q, n_tokens: int, out, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().kvq_chunk_step(handle, _ptr(k), _ptr(v), _ptr(q), n_tokens, _ptr(out), _ptr(workspace),
+                                workspace_bytes, _stream(stream)), "kvq_chunk_step")
+
+
+def kvq_copy_sequences(dst, src, index, stream=None) -> None:
+    _check(lib().kvq_copy_sequences(dst, src, _ptr(index), _stream(stream)), "kvq_copy_sequences")
+
+
+def kvq_buffers(handle) -> kvq_device_view:
+    view = kvq_device_view()
+    _check(lib().kvq_buffers(handle, ctypes.byref(view)), "kvq_buffers")
+    return view
+
+
 def kvq_axis_quantize(x, n_units, n_tokens, head_dim, bits, group_size, axis, codes, zero, scale, stream=None):
     _check(lib().kvq_axis_quantize(_ptr(x), n_units, n_tokens, head_dim, bits, group_size, axis, _ptr(codes),
                                    _ptr(zero), _ptr(scale), _stream(stream)), "kvq_axis_quantize")
@@ -303,7 +362,89 @@ def kvq_axis_attention(k, v, kv_f32, q, n_units, heads_per_unit, n_tokens, head_
                                     softmax_scale, _ptr(scores), _ptr(out), _stream(stream)), "kvq_axis_attention")
 
 
+# ------------------------------------------------------------------ rotary positions
+
+KVQ_TYPE_F16, KVQ_TYPE_BF16, KVQ_TYPE_F32 = 0, 1, 2
+ROPE_SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "yarn": 3}
+
+
+def make_rope_config(head_dim=128, rot_dim=None, base=10000.0, interleaved=False, scaling="none", factor=1.0, low=None,
+                     high=None, attention_factor=None, original_context=0) -> kvq_rope_config:
+    """Rotary positions of heads of head_dim channels (see kvq_rope_config in include/kvq.h).
+
+    The turns between which long-context scaling blends default to 1 and 4 ("wavelength") or 1 and 32 ("yarn"), the
+    factor on cosine and sine to 1, or 0.1 ln(factor) + 1 with "yarn".
+    """
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if attention_factor is None:
+        attention_factor = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
+    return kvq_rope_config(head_dim, head_dim if rot_dim is None else rot_dim, int(bool(interleaved)),
+                           ROPE_SCALINGS[scaling], base, factor, 1.0 if low is None else low,
+                           (32.0 if scaling == "yarn" else 4.0) if high is None else high, attention_factor,
+                           original_context)
+
+
+def kvq_rope(cfg: kvq_rope_config, parts, x_type: int, out_type: int, batch: int, n_tokens: int, positions, position0: int,
+             stream=None) -> None:
+    """parts: a sequence of kvq_rope_part; positions: device int64 [batch][n_tokens] or None."""
+    arr = (kvq_rope_part * len(parts))(*parts)
+    _check(lib().kvq_rope(ctypes.byref(cfg), arr, len(parts), x_type, out_type, batch, n_tokens, _ptr(positions), position0,
+                          _stream(stream)), "kvq_rope")
+
+
+def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out_dtype=None, stream=None):
+    """Rotary positions of up to four tensors [B, n, H, D] (any strides, channels contiguous) in one launch.
+
+    positions: the position of token 0 (token t stands at positions + t), or an int64 CUDA tensor [B, n].
+    rotate:    one truth value per tensor (default: all turned); a tensor that is not turned is moved along.
+    outs:      tensors [B, H, n, D] to write, or None for new contiguous ones of out_dtype (default fp16), the form the
+               cache takes.  An out may be its input's own memory.
+    """
+    import torch
+    types = {torch.float16: KVQ_TYPE_F16, torch.bfloat16: KVQ_TYPE_BF16, torch.float32: KVQ_TYPE_F32}
+    tensors = list(tensors)
+    rotate = [True] * len(tensors) if rotate is None else list(rotate)
+    if not tensors or len(rotate) != len(tensors) or (outs is not None and len(outs) != len(tensors)):
+        raise ValueError("need one to four tensors, and as many entries of rotate and outs")
+    x0 = tensors[0]
+    if not isinstance(x0, torch.Tensor) or x0.dim() != 4:
+        raise ValueError("need tensors [B, n, H, D]")
+    B, n, D = x0.shape[0], x0.shape[1], cfg.head_dim
+    if outs is None:
+        outs = [torch.empty((B, t.shape[2], n, D), dtype=out_dtype or torch.float16, device=x0.device) for t in tensors]
+    for name, group, dtype in (("tensors", tensors, x0.dtype), ("outs", outs, outs[0].dtype)):
+        for t, x in zip(group, tensors):
+            want = (B, n, x.shape[2], D) if name == "tensors" else (B, x.shape[2], n, D)
+            if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != x0.device or t.dtype != dtype
+                    or t.dtype not in types or tuple(t.shape) != want or t.stride(-1) != 1):
+                raise ValueError(f"{name}: need CUDA tensors {want} of one device and type (fp16, bf16 or fp32) with "
+                                 f"contiguous channels, got {t.device} {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    pos, pos0 = None, 0
+    if isinstance(positions, torch.Tensor):
+        if (positions.dtype != torch.int64 or positions.device != x0.device or tuple(positions.shape) != (B, n)
+                or not positions.is_contiguous()):
+            raise ValueError(f"positions: need a contiguous int64 tensor ({B}, {n}) on {x0.device}, or an integer")
+        pos = positions
+    else:
+        pos0 = int(positions)
+    parts = [kvq_rope_part(x.data_ptr(), o.data_ptr(), x.stride(0), x.stride(1), x.stride(2), o.stride(0), o.stride(2),
+                           o.stride(1), x.shape[2], int(bool(r))) for x, o, r in zip(tensors, outs, rotate)]
+    with torch.cuda.device(x0.device):
+        kvq_rope(cfg, parts, types[x0.dtype], types[outs[0].dtype], B, n, pos, pos0, _stream(stream, x0.device))
+    return outs
+
+
 # ------------------------------------------------------------------ owner object
+
+class _DeviceMemory:
+    """Device memory of a cache as an array that torch can view; holds the cache, so the memory outlives the view."""
+
+    def __init__(self, owner, ptr, shape, typestr):
+        self._owner = owner
+        self.__cuda_array_interface__ = {"shape": shape, "typestr": typestr, "data": (ptr, False), "version": 3,
+                                         "strides": None, "stream": None}
+
 
 class KVCache:
     """One layer's quantized KV cache on one GPU (torch tensors in, torch tensors out)."""
@@ -368,6 +509,77 @@ class KVCache:
         self._need(out, (c.batch, c.num_q_heads, c.head_dim), "out")
         kvq_decode_step(self.handle, k, v, q, out, _stream(stream, self.device))
         return out
+
+    def append_chunk(self, k, v, n_tokens=None, stream=None):
+        """Append the first n_tokens (default: all) of the tokens in k and v [B, Hkv, n, D]."""
+        c = self.cfg
+        n = k.shape[2]
+        self._need(k, (c.batch, c.num_kv_heads, n, c.head_dim), "k")
+        self._need(v, (c.batch, c.num_kv_heads, n, c.head_dim), "v")
+        kvq_append_chunk(self.handle, k, v, n if n_tokens is None else n_tokens, n, _stream(stream, self.device))
+
+    def chunk_workspace(self, n_tokens):
+        """Workspace for chunks of up to n_tokens tokens (a torch tensor; layers run in order share one)."""
+        import torch
+        return torch.empty(kvq_chunk_workspace(self.handle, n_tokens), dtype=torch.uint8, device=f"cuda:{self.device}")
+
+    def _chunk(self, call, k, v, q, out, workspace, stream):
+        import torch
+        c = self.cfg
+        n = q.shape[2] if q.dim() == 4 else 0
+        self._need(k, (c.batch, c.num_kv_heads, n, c.head_dim), "k")
+        self._need(v, (c.batch, c.num_kv_heads, n, c.head_dim), "v")
+        self._need(q, (c.batch, c.num_q_heads, n, c.head_dim), "q")
+        if out is None:
+            out = torch.empty_like(q)
+        self._need(out, (c.batch, c.num_q_heads, n, c.head_dim), "out")
+        if workspace is None:
+            workspace = self.chunk_workspace(n)
+            if stream is not None and not isinstance(stream, int):
+                workspace.record_stream(stream)
+            elif stream is not None:
+                workspace.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+        if (not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous()):
+            raise ValueError("workspace: need a contiguous CUDA tensor on the cache's device")
+        call(self.handle, k, v, q, n, out, workspace, workspace.numel() * workspace.element_size(),
+             _stream(stream, self.device))
+        return out
+
+    def chunk_attention(self, k, v, q, out=None, workspace=None, stream=None):
+        """Attention of a chunk of n new tokens (k, v [B, Hkv, n, D], q [B, Hq, n, D]) over the cached tokens and,
+        causally, over each other; the cache is not changed."""
+        return self._chunk(kvq_chunk_attention, k, v, q, out, workspace, stream)
+
+    def chunk_step(self, k, v, q, out=None, workspace=None, stream=None):
+        """chunk_attention(k, v, q), then append_chunk(k, v)."""
+        return self._chunk(kvq_chunk_step, k, v, q, out, workspace, stream)
+
+    def copy_sequences(self, src, index, stream=None):
+        """Make sequence b of this cache a copy of sequence index[b] of src (a KVCache; may be this one), for every b;
+        index: int32 CUDA tensor [batch]."""
+        import torch
+        if not isinstance(src, KVCache):
+            raise TypeError("src must be a KVCache")
+        if (not isinstance(index, torch.Tensor) or index.dtype != torch.int32 or not index.is_cuda
+                or index.device.index != self.device or tuple(index.shape) != (self.cfg.batch,)
+                or not index.is_contiguous()):
+            raise ValueError(f"index: need a contiguous int32 tensor ({self.cfg.batch},) on cuda:{self.device}")
+        kvq_copy_sequences(self.handle, src.handle, index, _stream(stream, self.device))
+
+    def buffers(self):
+        """The cache's device buffers as torch tensors over its own memory: pages uint8 [units, pages * page_bytes], wk
+        and wv fp16 [units, S + R, D] (sink rows, then window rows)."""
+        import torch
+        v = kvq_buffers(self.handle)
+        dev = f"cuda:{self.device}"
+        if v.pages_per_unit:
+            pages = torch.as_tensor(_DeviceMemory(self, v.pages, (v.n_units, v.pages_per_unit * v.page_bytes), "|u1"),
+                                    device=dev)
+        else:
+            pages = torch.empty((v.n_units, 0), dtype=torch.uint8, device=dev)
+        rows = [torch.as_tensor(_DeviceMemory(self, p, (v.n_units, v.rows_per_unit, self.cfg.head_dim), "<f2"), device=dev)
+                for p in (v.wk, v.wv)]
+        return {"pages": pages, "wk": rows[0], "wv": rows[1]}
 
     def reset(self):
         kvq_reset(self.handle)

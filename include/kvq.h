@@ -184,6 +184,67 @@ kvq_status kvq_decode_step(kvq_cache* cache, const void* k_f16, const void* v_f1
                            void* cuda_stream);
 
 /*
+ * Append n_tokens tokens at once: the state n_tokens kvq_append calls leave, bit for bit, in at most
+ * a few launches (the open window is filled and flushed, whole pages are quantized straight from k
+ * and v, the rest goes to the window).  k and v device fp16 [B][Hkv][src_tokens][D]; the first
+ * n_tokens of the src_tokens tokens of every row block are taken, 1 <= n_tokens <= src_tokens, so the accepted
+ * head of a drafted chunk is appended from the buffers the chunk was attended from.  Allowed in any
+ * state; KVQ_ERR_CAPACITY, before any work, when the tokens do not fit.
+ */
+kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_f16, const void* v_f16, int64_t n_tokens,
+                            int64_t src_tokens, void* cuda_stream);
+
+/*
+ * Attention of a chunk of n_tokens new tokens per sequence: k, v device fp16 [B][Hkv][n_tokens][D], q and out device
+ * fp16 [B][Hq][n_tokens][D].  Token i of the chunk attends the T cached tokens (as kvq_decode_attention
+ * sees them) and the chunk's own tokens 0..i, whose keys and values are taken in fp16 from k and v:
+ *   out[b][h][i] = softmax(scale * q[b][h][i] . [K_cache; k_0..k_i]^T) . [V_cache; v_0..v_i].
+ * The cache is not changed: kvq_append_chunk adds the chunk, or the part of it that was accepted,
+ * afterwards.  T = 0 is allowed and is the causal attention of a whole prompt.  With rope = 1 the
+ * chunk's keys arrive pre-RoPE like every key of such a cache and are rotated at positions T..T+n-1;
+ * q arrives rotated.  n_tokens >= 1, T + n_tokens < 2^31; whether the tokens fit the cache is not checked here.
+ *
+ * Keys and values are expanded to fp16 for the tensor cores (keys as differences from a per-channel
+ * offset that cancels in the softmax, or as a high and a low half when they are rotated), products
+ * accumulate in fp32, the softmax statistics are fp32, and the weights are rounded to fp16 before
+ * the value product.  Sums are taken in a fixed order: outputs are bitwise reproducible.  A cached or
+ * new token that a query does not attend cannot change its output, whatever it holds.
+ *
+ * workspace: device memory of at least kvq_chunk_workspace bytes, 16-byte aligned; it holds partial
+ * results of one call, so calls that may overlap on the GPU (other streams, graphs replayed at the
+ * same time) need one each, while calls in order on one stream -- all layers of a model -- share it.
+ * KVQ_ERR_INVALID_ARG when it is null or too small.
+ */
+kvq_status kvq_chunk_attention(kvq_cache* cache, const void* k_f16, const void* v_f16, const void* q_f16,
+                               int64_t n_tokens, void* out_f16, void* workspace, int64_t workspace_bytes,
+                               void* cuda_stream);
+
+/* One step of a layer over a chunk: kvq_chunk_attention, then kvq_append_chunk of all its tokens.
+   KVQ_ERR_CAPACITY before any work when the tokens do not fit. */
+kvq_status kvq_chunk_step(kvq_cache* cache, const void* k_f16, const void* v_f16, const void* q_f16, int64_t n_tokens,
+                          void* out_f16, void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
+/* Bytes of workspace that a chunk of up to n_tokens tokens needs on this cache, whatever it holds. */
+kvq_status kvq_chunk_workspace(const kvq_cache* cache, int64_t n_tokens, int64_t* bytes);
+
+/*
+ * Sequence b of dst becomes a copy of sequence index[b] of src, for every b of dst's batch: pages in
+ * use, fp16 window and sink rows, bit for bit, and dst takes over src's token counts.  Forks a
+ * prompt into samples (src of batch 1), compacts a batch after sequences ended (dst of a smaller
+ * batch), grows one, or, with dst == src, reorders beams in place under any map (cycles and repeated
+ * sources included).  index is a device int32 array of dst's batch size, 4-byte aligned, read when
+ * the copy runs, so a captured graph replays with the indices of the moment.  An entry outside
+ * [0, src batch) leaves its sequence's memory as it was and is recorded in dst's error word
+ * (kvq_sync_status of dst then reports KVQ_ERR_CUDA).
+ *
+ * The two configurations must agree in everything but batch and max_tokens, and so must the
+ * codebooks (KVQ_ERR_INVALID_ARG); both caches must be on one device.  KVQ_ERR_CAPACITY when dst
+ * cannot hold src's tokens; KVQ_ERR_STATE for a codebook cache without levels; KVQ_ERR_UNSUPPORTED in place beyond 14,528
+ * sequences.  The call uses both caches on this stream, and launches nothing when src is empty.
+ */
+kvq_status kvq_copy_sequences(kvq_cache* dst, kvq_cache* src, const int32_t* index, void* cuda_stream);
+
+/*
  * Codebooks of a cache created with codebook = 1: k_levels[0 .. 2^k_bits) and v_levels[0 .. 2^v_bits),
  * host fp32 arrays (copied), the level of each code in quantization steps, strictly increasing from
  * lev[0] = 0 to lev[L] = L (L = 2^bits - 1), so a group's minimum and maximum stay exact.  A value
@@ -342,6 +403,21 @@ typedef struct {
   int64_t sink_bytes;
 } kvq_unit_view;
 
+/*
+ * Device buffers of a cache, for callers that hand its pages on (kvq_decode_attention_noalloc, a
+ * checkpoint, another process): pages [B*Hkv][pages_per_unit][page_bytes] in the layout of
+ * kvq_page_layout, and the fp16 rows wk, wv [B*Hkv][rows_per_unit][D]: S sink rows, then the R rows of
+ * the window.  The buffers stay the cache's; they live until kvq_destroy.
+ */
+typedef struct {
+  void* pages;
+  void* wk;
+  void* wv;
+  int64_t pages_per_unit, page_bytes, rows_per_unit, n_units;
+} kvq_device_view;
+
+kvq_status kvq_buffers(const kvq_cache* cache, kvq_device_view* view);
+
 /* Fill the *_bytes fields of `sizes` for the current state (pointers untouched). */
 kvq_status kvq_unit_sizes(const kvq_cache* cache, kvq_unit_view* sizes);
 
@@ -405,6 +481,59 @@ const char* kvq_status_string(kvq_status status);
 
 /* Library version, (major << 16) | minor. */
 int32_t kvq_version(void);
+
+/* ---------------- rotary positions of new tokens ----------------
+ *
+ * The cache takes keys (rope = 0) and queries already rotated, as fp16 [B][H][n][D].  kvq_rope brings
+ * them there from wherever a projection left them: it turns the heads of up to four tensors at their
+ * tokens' positions, moves others along unturned (values; keys of a rope = 1 cache) and writes each
+ * in the layout and type asked for, in one launch on caller-owned buffers of the current device.
+ * Nothing is allocated.  ("Rotary embeddings complicate keys" on the unite.ai page fixes where the
+ * rotation belongs, not its variants.)
+ */
+#define KVQ_TYPE_F16 0
+#define KVQ_TYPE_BF16 1
+#define KVQ_TYPE_F32 2
+
+#define KVQ_ROPE_NONE 0       /* w_i = base^(-2i/rot_dim) */
+#define KVQ_ROPE_LINEAR 1     /* w_i / factor (positions interpolated) */
+#define KVQ_ROPE_WAVELENGTH 2 /* by turns u = original_context * w_i / (2 pi): w_i / factor up to `low` turns, w_i from
+                                 `high` on, blended linearly in u between */
+#define KVQ_ROPE_YARN 3       /* blended linearly in the pair's index between the pairs of `high` and `low` turns
+                                 (rounded outwards) */
+
+typedef struct {
+  int32_t head_dim;         /* D: even, at most 256 */
+  int32_t rot_dim;          /* channels [0, rot_dim) of a head are turned: even, 2..head_dim */
+  int32_t interleaved;      /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  int32_t scaling;          /* KVQ_ROPE_* */
+  double base;              /* > 1 */
+  double factor;            /* > 0; context extension, unused with KVQ_ROPE_NONE */
+  double low, high;         /* turns, 0 < low < high (KVQ_ROPE_WAVELENGTH, KVQ_ROPE_YARN) */
+  double attention_factor;  /* > 0; multiplies cosine and sine (1, or e.g. 0.1 ln(factor) + 1 with YARN) */
+  int64_t original_context; /* >= 1 (KVQ_ROPE_WAVELENGTH, KVQ_ROPE_YARN) */
+} kvq_rope_config;
+
+typedef struct {
+  const void* x;            /* device, x_type: element (b, t, h, c) at x + b*x_batch_stride + t*x_token_stride + h*x_head_stride + c */
+  void* out;                /* device, out_type, likewise; may be x itself (same type and strides), must not overlap otherwise */
+  int64_t x_batch_stride, x_token_stride, x_head_stride;       /* elements */
+  int64_t out_batch_stride, out_token_stride, out_head_stride; /* elements */
+  int32_t num_heads;
+  int32_t rotate;           /* 1: turned, 0: moved (and converted) only */
+} kvq_rope_part;
+
+/*
+ * out = rotation of x for parts[0 .. n_parts), n_parts <= 4, tokens b < batch, t < n_tokens, at positions[b][t]
+ * (device int64 [batch][n_tokens], 8-byte aligned) or, when positions is NULL, position0 + t.  Positions may be any
+ * 64-bit numbers (negative ones turn the other way).  Pair i with values (x_a, x_b), t = pos * w_i and m =
+ * attention_factor becomes (m (x_a cos t - x_b sin t), m (x_a sin t + x_b cos t)), computed in fp32 with the angle
+ * modulo one turn exact for positions beyond 2^24, and rounded once to out_type.  Rows that are 16-byte aligned with
+ * head_dim and rot_dim multiples of 16 take 16-byte accesses; any other element-aligned layout works.
+ */
+kvq_status kvq_rope(const kvq_rope_config* cfg, const kvq_rope_part* parts, int32_t n_parts, int32_t x_type,
+                    int32_t out_type, int32_t batch, int64_t n_tokens, const int64_t* positions, int64_t position0,
+                    void* cuda_stream);
 
 /* ---------------- axis ablation (analysis beside the cache, not the cache) ----------------
  *
