@@ -470,6 +470,8 @@ kvq_status launch_chunk_for(kvq_cache* c, const void* k, const void* v, const vo
     std::memcpy(p.k_lev, c->k_lev, sizeof(p.k_lev));
     std::memcpy(p.v_lev, c->v_lev, sizeof(p.v_lev));
   }
+  p.wait_ns = c->test_wait_ns;
+  p.test_withhold = c->test_withhold;
   int launches = 0;
   const cudaError_t e = kvq::launch_chunk(p, c->cfg.rope != 0, c->sm_count, workspace, &launches, s);
   c->launches += launches;

@@ -5,18 +5,21 @@
 // chunk's tokens up to i.  One pass over the keys with a running maximum m and sum l per query row
 // (base 2; the maximum is renewed, and the accumulator rescaled, only when it rises by more than 2^8).
 //
-// Work list.  A job is 128 query rows of one (sequence, kv head) unit -- the chunk's tokens with the heads
-// that share the kv head beside each other, so grouped heads fill the tile -- and a tile is up to 128
-// keys: whole pages first, then the unit's fp16 rows (sink, window) followed by the new tokens as far
-// as the job's last token sees.  The flat list of all jobs' tiles is cut into equal contiguous pieces,
-// one per CTA, so few rows over a long cache are spread over the whole GPU and many rows leave no
+// Work list.  A job is up to 256 query rows of one (sequence, kv head) unit -- the chunk's tokens with the
+// heads that share the kv head beside each other, so grouped heads fill the tiles -- and a tile is up
+// to 128 keys: whole pages first, then the unit's fp16 rows (sink, window) followed by the new tokens as
+// far as the job's last token sees.  The flat list of all jobs' tiles is cut into equal contiguous
+// pieces, one per SM, so few rows over a long cache are spread over the whole GPU and many rows leave no
 // partly filled last wave.  A job that a cut divides leaves unnormalised partials (m, l, acc) in the
 // workspace, at most two per CTA, and merge_chunk_kernel joins them in CTA order.
 //
-// A tile.  All warps expand codes into fp16 operand tiles in shared memory; one thread issues
-// S = Q K^T (128 x 128 x 128) into tensor memory; four warps, a thread per query row, turn S into P (fp16,
-// back into tensor memory over S); one thread issues O += P V.  Two CTAs per SM overlap one's
-// expansion with the other's products.
+// A CTA.  Eight producer warps expand codes into fp16 operand tiles in shared memory (four for keys, four
+// for values), one thread issues the products, and two groups of four warps, a thread per query row, turn
+// S = Q K^T into P (fp16, back into tensor memory over S).  The two groups are two streams whose products
+// alternate, PV of one after QK of the other, so the tensor cores work on one stream while the other is in
+// its softmax.  With more than 128 rows the streams are the two halves of the rows over the same key
+// tiles; with up to 128 they are the even and the odd key tiles of the same rows, joined at the end
+// through shared memory.
 //
 // Operand precision.  Every product is fp16 x fp16 with fp32 accumulation.  A dequantized key z + s c has up
 // to 15 significant bits and, in outlier channels, a magnitude of tens, whose fp16 rounding would cost
@@ -26,6 +29,8 @@
 // rounding.  Rotated keys have no such constant: they enter as hi + lo, two fp16 halves and two
 // products (22 bits).  Weights are rounded to fp16 scaled by 2^7, so a weight down to 2^-31 of the
 // maximum still counts; values z + s c are rounded once.
+#include <cstddef>
+
 #include <cuda_fp16.h>
 
 #include "kvq_internal.h"
@@ -36,22 +41,28 @@ namespace kvq {
 namespace {
 
 constexpr int kD = kHeadDim;
-constexpr int kRows = 128;   // query rows of a job
+constexpr int kRows = 128;   // query rows of a stream
 constexpr int kTile = 128;   // keys of a tile
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kProducers = 4;  // warps that make key tiles, and as many that make value tiles
+constexpr int kThreads = (8 + 2 * kProducers + 1) * 32;
 constexpr float kLazy = 8.0f;      // log2 units the running maximum may lag behind
 constexpr float kWeightExp = 7.0f; // weights are at most 2^(8 + 7): below fp16's 65504
-constexpr int kTmemColumns = 256;  // S / P: 0..127, O: 128..255
+constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O at 256 and 384
+constexpr int kValueStages = 2;
+constexpr int kBadSlots = 4;       // marks of non-finite values: producers run at most three jobs ahead
 
-struct Shared {
-  uint64_t bar;
+struct __align__(16) Shared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], x_written, x_read, k_sync, v_sync;
   uint32_t tmem;
-  int bad;                    // some token of the tile has a non-finite value (see patch_values)
-  uint32_t bad_tokens[4];
-  __half2 mu[kD / 2];         // per channel pair
+  uint32_t bad[kBadSlots][8];  // tokens of the job with a non-finite value that some of its rows must not see
+  __half2 mu[kD / 2];          // per channel pair
+  alignas(16) uint32_t k_meta[2][kProducers][128], v_meta[2][kProducers][128];  // zero points and steps of two tiles' blocks
   float k_lev[16], v_lev[16];
+  float xm[kRows], xl[kRows];  // the second stream's m and l
 };
+
+static_assert(offsetof(Shared, k_meta) % 16 == 0 && offsetof(Shared, v_meta) % 16 == 0, "16-byte asynchronous copies");
 
 // Row of the value tile (and column of O) that holds channel d: the low bit of d moves to bit 2 within
 // groups of eight, which spreads the page producer's 16-byte stores over all banks.
@@ -60,13 +71,15 @@ __device__ __forceinline__ int value_row(int d) { return (d & ~7) | ((d & 1) << 
 // ------------------------------------------------------------ work list
 
 // fp16 tiles of the first `jobs` jobs of a unit: sum over k = 1..jobs of ceil((n_w + k * job_tokens) / 128).
+// Job sizes are powers of two, so the terms repeat with a fixed step after max(1, 128 / job_tokens) jobs.
 __host__ __device__ inline int64_t f16_tiles_before(int64_t n_w, int log2_job_tokens, int64_t jobs) {
-  const int period = 1 << (7 - log2_job_tokens);  // jobs per 128 tokens
-  const int64_t m = jobs / period, rem = jobs - m * period;
+  const int lp = log2_job_tokens < 7 ? 7 - log2_job_tokens : 0;            // log2 of the jobs in a period
+  const int64_t step = log2_job_tokens > 7 ? 1 << (log2_job_tokens - 7) : 1;  // tiles a period adds
+  const int64_t m = jobs >> lp, rem = jobs - (m << lp);
   int64_t sum = 0;
-  for (int i = 1; i <= period; ++i) {
+  for (int i = 1; i <= (1 << lp); ++i) {
     const int64_t c = (n_w + ((int64_t)i << log2_job_tokens) + 127) >> 7;
-    sum += m * c + m * (m - 1) / 2 + (i <= rem ? c + m : 0);
+    sum += m * c + step * (m * (m - 1) / 2) + (i <= rem ? c + step * m : 0);
   }
   return sum;
 }
@@ -79,7 +92,7 @@ struct Piece {
   int tokens;                // chunk tokens of the job
 };
 
-__host__ __device__ inline Piece find_piece(const ChunkParams& p, int64_t g) {
+__host__ __device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t g) {
   Piece x;
   x.unit = g / p.tiles_per_unit;
   const int64_t r = g - x.unit * p.tiles_per_unit;
@@ -125,37 +138,44 @@ __device__ __forceinline__ __half2 code_pair(uint32_t word, int j) {
   return __hfma2(h2(x), __float2half2_rn(inv), __float2half2_rn(-1024.0f * inv));
 }
 
+// Codes of a 32-token block of a fragment-order page: two 16-token tiles of 2B words per lane.
+template <int B>
+__device__ __forceinline__ void load_codes(const uint8_t* codes, int block, int lane, uint32_t (&w)[4 * B]) {
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const uint4* src = reinterpret_cast<const uint4*>(codes) + ((2 * block + a) * 32 + lane) * (B / 2);
+#pragma unroll
+    for (int i = 0; i < B / 2; ++i) {
+      const uint4 v = __ldg(src + i);
+      w[2 * B * a + 4 * i] = v.x;
+      w[2 * B * a + 4 * i + 1] = v.y;
+      w[2 * B * a + 4 * i + 2] = v.z;
+      w[2 * B * a + 4 * i + 3] = v.w;
+    }
+  }
+}
+
 // Keys of a 32-token block of a fragment-order page, for one warp.  Lane l = 4g + t holds, per token
 // row, the 32 channels 8i + 2t + {0, 1}; the key tile's column order puts them side by side
 // (column 64 (i/8) + 16 t + 8 ((i/4) % 2) + 2 (i % 4) + {0, 1}; the queries are stored in the same order), so every
 // store is 16 bytes and eight neighbouring lanes hit all banks.  Key rows take the token order
-// 16a + 8b + 2t' + e -> 8t' + 4a + 2b + e that the value block's words come in.
+// 16a + 8b + 2t' + e -> 8t' + 4a + 2b + e that the value block's words come in.  meta: the group's 128
+// zero point / step words in shared memory.
+//
+// The loop over the channels is kept a loop (the words are shifted along as it goes): the five roles of a
+// CTA run different code side by side, and unrolled bodies miss the instruction caches -- the unrolled
+// form of this kernel spent 4.6 of 13.6 cycles per issued instruction waiting for instructions.
 template <int B>
-__device__ __forceinline__ void key_block(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
-                                          int slot, uint32_t tile, int lane) {
+__device__ __forceinline__ void key_block(uint32_t (&w)[4 * B], const uint2* meta, const __half2* mu, int slot,
+                                          uint32_t tile, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  uint32_t w[2][2 * B];
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const uint4* src = reinterpret_cast<const uint4*>(page + p.lay.off_kc) + ((2 * block + a) * 32 + lane) * (B / 2);
-#pragma unroll
-    for (int i = 0; i < B / 2; ++i) {
-      const uint4 v = __ldg(src + i);
-      w[a][4 * i] = v.x;
-      w[a][4 * i + 1] = v.y;
-      w[a][4 * i + 2] = v.z;
-      w[a][4 * i + 3] = v.w;
-    }
-  }
-  const uint2* meta = reinterpret_cast<const uint2*>(page + p.lay.off_km) + (32 * block / p.G) * (kD / 2);
-#pragma unroll
+#pragma unroll 1
   for (int q = 0; q < 4; ++q) {  // 32 channels: i = 4q .. 4q + 3
     __half2 z[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int pair = 4 * (4 * q + k) + t;
-      const uint2 m = __ldg(meta + pair);
-      z[k] = __hsub2(h2(__byte_perm(m.x, m.y, 0x5410)), sh.mu[pair]);
+      const uint2 m = meta[4 * (4 * q + k) + t];
+      z[k] = __hsub2(h2(__byte_perm(m.x, m.y, 0x5410)), mu[4 * (4 * q + k) + t]);
       s[k] = h2(__byte_perm(m.x, m.y, 0x7632));
     }
 #pragma unroll
@@ -164,65 +184,61 @@ __device__ __forceinline__ void key_block(const ChunkParams& p, const Shared& sh
       for (int b = 0; b < 2; ++b) {
         uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int u = B == 2 ? q / 2 : q, j = B == 2 ? 4 * (q % 2) + k : k;
-          o[k] = u32(__hfma2(code_pair<B>(w[a][b * B + u], j), s[k], z[k]));
-        }
+        for (int k = 0; k < 4; ++k) o[k] = u32(__hfma2(code_pair<B>(w[2 * B * a + b * B], k), s[k], z[k]));
         const int row = 32 * slot + 8 * (g >> 1) + 4 * a + 2 * b + (g & 1);
-        sts16(tile + tc::chunk_offset(q / 2, row, 2 * t + (q & 1)), o[0], o[1], o[2], o[3]);
+        sts16(tile + tc::chunk_offset(q >> 1, row, 2 * t + (q & 1)), o[0], o[1], o[2], o[3]);
+      }
+    // the next 32 channels' codes: the upper half of a 2-bit word's pairs, or the next word
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        uint32_t& v = w[x * B + u];
+        if (B == 2) v = u == 0 ? ((q & 1) ? w[x * B + 1] : v >> 8) : v;
+        else v = u + 1 < B ? w[x * B + u + 1] : v;
       }
   }
 }
 
 // Values of a 32-token block of a fragment-order page, for one warp: the tile is [channel][token], and
-// a lane's words hold the token pairs that make 16 bytes of a channel's row.
+// a lane's words hold the token pairs that make 16 bytes of a channel's row.  meta: the block's
+// [32 tokens][D/G] zero point / step words in shared memory; half = 1 when G = 64.
 template <int B>
-__device__ __forceinline__ void value_block(const ChunkParams& p, const uint8_t* page, int block, int slot,
+__device__ __forceinline__ void value_block(uint32_t (&w)[4 * B], const uint32_t* meta, int half, int slot,
                                             uint32_t tile, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  uint32_t w[2][2 * B];
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const uint4* src = reinterpret_cast<const uint4*>(page + p.lay.off_vc) + ((2 * block + a) * 32 + lane) * (B / 2);
-#pragma unroll
-    for (int i = 0; i < B / 2; ++i) {
-      const uint4 v = __ldg(src + i);
-      w[a][4 * i] = v.x;
-      w[a][4 * i + 1] = v.y;
-      w[a][4 * i + 2] = v.z;
-      w[a][4 * i + 3] = v.w;
-    }
-  }
-  const uint32_t* meta = reinterpret_cast<const uint32_t*>(page + p.lay.off_vm);
-  const int per_token = kD / p.G, half = p.G == 64 ? 1 : 0;
-#pragma unroll
+  const int per_token = 4 >> half;
+#pragma unroll 1
   for (int q = 0; q < 4; ++q) {  // channels 32q .. 32q + 31
     __half2 z[2][2], s[2][2];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int tok = 32 * block + 16 * a + 8 * b + 2 * t;
-        const uint32_t m0 = __ldg(meta + tok * per_token + (q >> half));
-        const uint32_t m1 = __ldg(meta + (tok + 1) * per_token + (q >> half));
+        const uint32_t* m = meta + (16 * a + 8 * b + 2 * t) * per_token + (q >> half);
+        const uint32_t m0 = m[0], m1 = m[per_token];
         z[a][b] = h2(__byte_perm(m0, m1, 0x5410));
         s[a][b] = h2(__byte_perm(m0, m1, 0x7632));
       }
 #pragma unroll
-    for (int x = 2 * q; x < 2 * q + 2; ++x)
+    for (int x = 0; x < 2; ++x)  // channels 16 (2q + x) + 8r + g: pair 2q + x of word r
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         uint32_t o[4];
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int u = x / (16 / B), j = x % (16 / B);
-            o[2 * a + b] = u32(__hfma2(code_pair<B>(w[a][(2 * b + r) * (B / 2) + u], j), s[a][b], z[a][b]));
-          }
-        const int row = value_row(16 * x + 8 * r + g);
-        sts16(tile + tc::chunk_offset(slot / 2, row, 4 * (slot & 1) + t), o[0], o[1], o[2], o[3]);
+          for (int b = 0; b < 2; ++b)
+            o[2 * a + b] = u32(__hfma2(code_pair<B>(w[2 * B * a + (2 * b + r) * (B / 2)], x), s[a][b], z[a][b]));
+        const int row = value_row(32 * q + 16 * x + 8 * r + g);
+        sts16(tile + tc::chunk_offset(slot >> 1, row, 4 * (slot & 1) + t), o[0], o[1], o[2], o[3]);
       }
+    // the next 32 channels' pairs: two pairs down, and for 4-bit codes the second word after two steps
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      uint32_t& v = w[x * (B / 2)];
+      v = B == 4 && (q & 1) ? w[x * (B / 2) + B / 2 - 1] : v >> (2 * B);
+    }
   }
 }
 
@@ -300,7 +316,7 @@ template <bool ROPE>
 __device__ __forceinline__ void key_tile_bits(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
                                               int64_t page0, uint32_t tile, int warp, int lane) {
   const int bits = p.bk, mask = (1 << bits) - 1;
-  for (int task = warp; task < 32; task += kWarps) {
+  for (int task = warp; task < 32; task += kProducers) {
     const int q = task >> 2, tok = 32 * (task & 3) + lane;
     const int in_tile = tok / p.R;
     const int64_t page = page0 + in_tile;
@@ -344,7 +360,7 @@ __device__ __forceinline__ void key_tile_bits(const ChunkParams& p, const Shared
 __device__ __forceinline__ void value_tile_bits(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
                                                 int64_t page0, uint32_t tile, int warp, int lane) {
   const int bits = p.bv, mask = (1 << bits) - 1;
-  for (int task = warp; task < 32; task += kWarps) {
+  for (int task = warp; task < 32; task += kProducers) {
     const int q = task >> 1, tp = 32 * (task & 1) + lane, tok = 2 * tp;
     const int in_tile = tok / p.R;
     const int64_t page = page0 + in_tile;
@@ -372,7 +388,7 @@ __device__ __forceinline__ void value_tile_bits(const ChunkParams& p, const Shar
 // Sparse entries of fragment-order pages, over the dense keys already in the tile.
 __device__ __forceinline__ void sparse_keys(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
                                             int64_t page0, uint32_t tile, int tid) {
-  for (int i = tid; i < kTile * p.nsp; i += kThreads) {
+  for (int i = tid; i < kTile * p.nsp; i += kProducers * 32) {
     const int tok = i / p.nsp, e = i - tok * p.nsp;
     const int in_tile = tok / p.R;
     const int64_t page = page0 + in_tile;
@@ -399,21 +415,31 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
                                              const uint16_t* fresh, int64_t j0, int64_t end, uint32_t tile, int warp,
                                              int lane) {
   if constexpr (FRAG) {
-    for (int task = warp; task < 16; task += kWarps) {
-      const int row = 8 * task + (lane >> 2), q = lane & 3;
-      uint4 v[4] = {};
-      if (j0 + row < end) {
-        const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j0 + row)) + 4 * q;
-        uint32_t* x = reinterpret_cast<uint32_t*>(v);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // two rows' loads in flight per lane
+      uint4 v[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
+      for (int h = 0; h < 2; ++h) {
+        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane >> 2);
+        if (j0 + row < end) {
+          const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j0 + row)) + 4 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
+          for (int i = 0; i < 4; ++i) v[h][i] = __ldg(src + i);
+        }
       }
-      store_frag_row(tile, row, q, v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane >> 2), q = lane & 3;
+        uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
+        if (j0 + row < end) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
+        }
+        store_frag_row(tile, row, q, v[h]);
+      }
     }
   } else {
-    for (int task = warp; task < 32; task += kWarps) {
+    for (int task = warp; task < 32; task += kProducers) {
       const int q = task >> 2, row = 32 * (task & 3) + lane;
       const int64_t j = j0 + row;
       float x[8] = {}, y[8] = {};
@@ -436,61 +462,92 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
   }
 }
 
-// Values of an fp16 tile.  Tokens from `cut` on are hidden from some of the job's rows, and 0 * inf or
-// 0 * NaN would carry what they hold into those rows: non-finite values there enter the product as 0
-// and are marked, for patch_values to add to the rows that do see them.
-__device__ __forceinline__ void value_tile_f16(const ChunkParams& p, Shared& sh, const uint16_t* rows,
-                                               const uint16_t* fresh, int64_t j0, int64_t end, int64_t cut,
+// Values of an fp16 tile.  Tokens behind the job's first are hidden from some of its rows, and 0 * inf
+// or 0 * NaN would carry what they hold into those rows: non-finite values there enter the product as 0
+// and their tokens are marked, for patch_values to add them to the rows that do see them.
+__device__ __forceinline__ void value_tile_f16(const ChunkParams& p, uint32_t* bad, const uint16_t* rows,
+                                               const uint16_t* fresh, int64_t j0, int64_t end, int64_t job0,
                                                uint32_t tile, int warp, int lane) {
-  for (int task = warp; task < 32; task += kWarps) {
-    const int cp = 32 * (task & 1) + lane, o = task >> 1;  // channel pair, octet of tokens
-    uint32_t x[8];
+#pragma unroll 1
+  for (int batch = 0; batch < 4; ++batch) {
+    uint32_t x[2][8];  // two octets' loads in flight per lane
+    const int o = (warp >> 1) + 4 * batch, cp = 32 * (warp & 1) + lane;  // octets o and o + 2, channel pair
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t j = j0 + 8 * o + i;
-      x[i] = j < end ? __ldg(reinterpret_cast<const uint32_t*>(f16_row(rows, fresh, p.n_w, j)) + cp) : 0u;
-    }
-    if (j0 + 8 * o + 7 >= cut) {
+    for (int h = 0; h < 2; ++h) {
+      const int64_t j = j0 + 8 * (o + 2 * h);
+      if (j + 8 <= end && (j >= p.n_w || j + 8 <= p.n_w)) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(f16_row(rows, fresh, p.n_w, j)) + cp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool lo = (x[i] & 0x7C00u) == 0x7C00u, hi = (x[i] & 0x7C000000u) == 0x7C000000u;
-        if ((lo || hi) && j0 + 8 * o + i >= cut) {
-          x[i] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
-          x[i] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
-          sh.bad = 1;
-          atomicOr(&sh.bad_tokens[o >> 2], 1u << ((8 * o + i) & 31));
-        }
+        for (int i = 0; i < 8; ++i) x[h][i] = __ldg(src + i * (kD / 2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[h][i] = j + i < end ? __ldg(reinterpret_cast<const uint32_t*>(f16_row(rows, fresh, p.n_w, j + i)) + cp) : 0u;
       }
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t sel = e ? 0x7632 : 0x5410;
-      sts16(tile + tc::chunk_offset(o >> 3, value_row(2 * cp + e), o & 7), __byte_perm(x[0], x[1], sel),
-            __byte_perm(x[2], x[3], sel), __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
+    for (int h = 0; h < 2; ++h) {
+      const int oct = o + 2 * h;
+      if (j0 + 8 * oct + 7 > job0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool lo = (x[h][i] & 0x7C00u) == 0x7C00u, hi = (x[h][i] & 0x7C000000u) == 0x7C000000u;
+          if (lo || hi) {
+            const int64_t rel = j0 + 8 * oct + i - job0;  // token of the job
+            if (rel > 0) {
+              x[h][i] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
+              x[h][i] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
+              atomicOr(&bad[rel >> 5], 1u << (rel & 31));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t sel = e ? 0x7632 : 0x5410;
+        sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + e), oct & 7), __byte_perm(x[h][0], x[h][1], sel),
+              __byte_perm(x[h][2], x[h][3], sel), __byte_perm(x[h][4], x[h][5], sel), __byte_perm(x[h][6], x[h][7], sel));
+      }
     }
   }
 }
 
-// Add p_j v_j for the marked non-finite values of a tile to the rows that see token j (rare and slow).
-__device__ __noinline__ void patch_values(const ChunkParams& p, const Shared& sh, const uint16_t* rows,
-                                          const uint16_t* fresh, int64_t j0, int limit, uint32_t tmem) {
-  for (int j = 0; j < kTile; ++j) {
-    if (!((sh.bad_tokens[j >> 5] >> (j & 31)) & 1u)) continue;
-    const uint32_t pair = tc::ld1(tmem + j / 2);
-    tc::wait_ld();
-    const float w = __half2float(j & 1 ? __high2half(h2(pair)) : __low2half(h2(pair)));
-    const uint16_t* v = f16_row(rows, fresh, p.n_w, j0 + j);
-    for (int c = 0; c < kD; ++c) {
-      const float f = __half2float(__ushort_as_half(v[c]));
-      if (isfinite(f)) continue;
-      const uint32_t at = tmem + kTile + value_row(c);
-      const uint32_t acc = tc::ld1(at);
-      tc::wait_ld();
-      const float sum = __uint_as_float(acc) + w * f;
-      tc::st1(at, j < limit ? __float_as_uint(sum) : acc);
-      tc::wait_st();
+// What the marked tokens up to the row's own add to its channels 32y .. 32y + 31: their non-finite values
+// (every visible token has a positive weight, so inf or NaN is the sum's).  `o` is in value_row order.
+__device__ __noinline__ void patch_values(const uint32_t* bad, const uint16_t* job_v, int token, int y, uint32_t* o) {
+  for (int i = 1; i <= token; ++i) {
+    if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
+    for (int c = 0; c < 32; ++c) {
+      const float f = __half2float(__ushort_as_half(job_v[(int64_t)i * kD + 32 * y + c]));
+      if (!isfinite(f)) o[value_row(c)] = __float_as_uint(__uint_as_float(o[value_row(c)]) + f);
     }
   }
+}
+
+// Two fp32 numbers in a 64-bit register, and the packed forms of multiply-add and add.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -501,71 +558,123 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ------------------------------------------------------------ the kernel
 
-// BK, BV: code widths of fragment-order pages, or 0 for bitstream pages (widths at run time).
-template <int BK, int BV, bool ROPE>
-__global__ void __launch_bounds__(kThreads, ROPE ? 1 : 2) chunk_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr bool FRAG = BK != 0;
-  extern __shared__ uint8_t raw[];
-  __shared__ Shared sh;
-  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + tc::kTileBytes, sv = sk + (ROPE ? 2 : 1) * tc::kTileBytes;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+template <bool ROPE>
+constexpr int kKeyStages = ROPE ? 1 : 2;  // a rotated key tile is two tiles, hi and lo
+template <bool ROPE>
+constexpr int kKeyBytes = (ROPE ? 2 : 1) * tc::kTileBytes;
+template <bool ROPE>
+constexpr int kSmemBytes = 2 * tc::kTileBytes + kKeyStages<ROPE> * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
 
-  if (tid == 0) {
-    mbar_init(&sh.bar, 1);
-    fence_mbar_init();
+// A CTA's walk over its pieces of the work list: what every role needs to know of one.
+struct Walk {
+  Piece x;
+  int64_t t_begin, t_end;  // tiles of the job in this piece
+  bool dual;               // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
+  int rows;
+  __device__ __forceinline__ void at(const ChunkParams& p, int64_t g, int64_t g_end) {
+    x = find_piece(p, g);
+    t_begin = g - x.job_start;
+    const int64_t left = t_begin + (g_end - g);
+    t_end = x.tiles < left ? x.tiles : left;
+    rows = x.tokens << p.log2hg;
+    dual = rows <= kRows;
   }
-  if (tid < 16) {
-    sh.k_lev[tid] = p.k_lev[tid];
-    sh.v_lev[tid] = p.v_lev[tid];
-  }
-  if (warp == 0) tc::alloc(&sh.tmem, kTmemColumns);
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tmem = sh.tmem;
-  const uint32_t my_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  pdl_allow_next();
+  __device__ __forceinline__ int64_t tiles() const { return t_end - t_begin; }
+};
 
-  uint32_t phase = 0;
-  bool failed = false;
-  const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
-  const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
-  const int hg = 1 << p.log2hg;
-  for (int64_t g = g_begin; g < g_end && !failed;) {
-    const Piece x = find_piece(p, g);
-    const int64_t t_begin = g - x.job_start;
-    const int64_t t_end = min(x.tiles, t_begin + (g_end - g));
-    const int64_t b = x.unit / p.Hkv, kvh = x.unit - b * p.Hkv;
-    const uint8_t* unit_pages = p.pages + x.unit * p.unit_page_stride;
-    const uint16_t* rows_k = p.wk + x.unit * p.win_unit_stride;
-    const uint16_t* rows_v = p.wv + x.unit * p.win_unit_stride;
-    const uint16_t* new_k = p.k_new + x.unit * p.n * kD;
-    const uint16_t* new_v = p.v_new + x.unit * p.n * kD;
-    const int rows = x.tokens << p.log2hg;
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit) {
+  return mbar_wait(bar, parity, limit ? limit : kWaitLimitNs);
+}
+__device__ __forceinline__ bool wait(const ChunkParams& p, uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, p.wait_ns);
+}
 
-    // queries: row r = token r / hg, head r % hg of the group; channels in the key tile's column order
-    for (int task = warp; task < 16; task += kWarps) {
-      const int r = 8 * task + (lane >> 2), q = lane & 3;
-      uint4 v[4] = {};
-      if (r < rows) {
-        const int64_t row = (b * p.Hq + kvh * hg + (r & (hg - 1))) * p.n + x.tok0 + (r >> p.log2hg);
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row * kD) + 4 * q;
+// Barrier among the warps of one role, with the time limit of every wait (a hardware barrier has none).
+__device__ __forceinline__ bool sync_role(const ChunkParams& p, uint64_t* bar, uint32_t* count) {
+  mbar_arrive(bar);
+  return wait(p, bar, (*count)++ & 1);
+}
+
+// One product of a stream with a tile: S = Q K^T (hi and lo halves of rotated keys), or O (+)= P V.
+template <bool ROPE>
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sq, uint32_t sk) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
+  for (int h = 0; h < (ROPE ? 2 : 1); ++h)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
+      tc::mma_ss(d, tc::descriptor(sq + off), tc::descriptor(sk + h * tc::kTileBytes + off), tc::instruction(kTile),
+                 h > 0 || k > 0);
+    }
+}
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint32_t sv, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
+    tc::mma_ts(d, pcol + 8 * k, tc::descriptor(sv + off), tc::instruction(kD), accumulate || k > 0);
+  }
+}
+
+// The issuing thread.  Step s of a piece is one stream's turn at one tile; QK runs two steps ahead of PV, so
+// between a stream's QK and its PV the tensor cores have the other stream's products.  P overlies S: QK of
+// step s + 2 comes behind PV of step s, which reads P, in issue order.
+template <bool ROPE>
+__device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sk, uint32_t sv,
+                                           uint32_t tmem, int64_t g_begin, int64_t g_end) {
+  constexpr int KS = kKeyStages<ROPE>;
+  uint32_t kt0 = 0, jobs = 0, used[2] = {0, 0};  // tiles and pieces so far, steps of each stream so far
+  for (int64_t g = g_begin; g < g_end; ++jobs) {
+    Walk w;
+    w.at(p, g, g_end);
+    const int tiles = (int)w.tiles(), steps = w.dual ? tiles : 2 * tiles;
+    if (!wait(p, &sh.q_full[0], jobs & 1) || !wait(p, &sh.q_full[1], jobs & 1)) return false;
+#pragma unroll 1
+    for (int s = -2; s < steps; ++s) {
+      const int q = s & 1;
+      const uint32_t at = 128 * q, kt = kt0 + (w.dual ? s : s >> 1);  // of step s; QK's tile is one or two on
+      if (s >= 0) {
+        const uint32_t st = kt % kValueStages;
+        if (!wait(p, &sh.v_full[st], (kt / kValueStages) & 1)) return false;
+        if (!wait(p, &sh.p_ready[q], used[q] & 1)) return false;
+        used[q]++;
+        tc::fence_after();
+        issue_pv(tmem + 256 + at, tmem + at, sv + st * tc::kTileBytes, s >= 2);
+        if (w.dual || q == 1) tc::commit(&sh.v_empty[st]);
+        if (s + 2 >= steps) tc::commit(&sh.o_done[q]);
       }
-      if constexpr (FRAG) {
-        store_frag_row(sq, r, q, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sts16(sq + tc::chunk_offset(q >> 1, r, 4 * (q & 1) + i), v[i].x, v[i].y, v[i].z, v[i].w);
+      if (s + 2 < steps) {
+        const uint32_t kn = kt + (w.dual ? 2 : 1), st = kn % KS;
+        if (!wait(p, &sh.k_full[st], (kn / KS) & 1)) return false;
+        tc::fence_after();
+        issue_qk<ROPE>(tmem + at, sq + (w.dual ? 0 : q * tc::kTileBytes), sk + st * kKeyBytes<ROPE>);
+        tc::commit(&sh.s_full[q]);
+        if (w.dual || q == 1) tc::commit(&sh.k_empty[st]);
       }
     }
-    // mu: the centre of each channel's range in one page of the unit
-    if (tid < kD) {
+    kt0 += tiles;
+    g += tiles;
+  }
+  return true;
+}
+
+// Key producers: warp 0..3.
+template <int BK, bool ROPE>
+__device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int64_t g_begin, int64_t g_end,
+                                         int warp, int lane) {
+  constexpr bool FRAG = BK != 0;
+  constexpr int KS = kKeyStages<ROPE>;
+  const int tid = 32 * warp + lane;
+  uint32_t kt = 0, syncs = 0;
+  for (int64_t g = g_begin; g < g_end;) {
+    Walk w;
+    w.at(p, g, g_end);
+    const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
+    const uint16_t* rows = p.wk + w.x.unit * p.win_unit_stride;
+    const uint16_t* fresh = p.k_new + w.x.unit * p.n * kD;
+    if constexpr (!ROPE) {  // mu: the centre of each channel's range in one page of the unit
+      if (!sync_role(p, &sh.k_sync, &syncs)) return false;  // the last piece's tiles no longer need the old one
       float mu = 0.0f;
-      if (!ROPE && p.n_pages > 0) {
+      if (p.n_pages > 0) {
         const uint8_t* pg = unit_pages + (p.n_pages / 2) * p.lay.bytes;
         const __half2 m = h2(reinterpret_cast<const uint32_t*>(pg + p.lay.off_km)[tid]);
         const float range = __high2float(m) * (float)((1 << p.bk) - 1);
@@ -573,191 +682,421 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 1 : 2) chunk_kernel(const __g
         if (fabsf(centre) > range && fabsf(centre) <= 4096.0f) mu = centre;
       }
       reinterpret_cast<__half*>(sh.mu)[tid] = __float2half_rn(mu);
+      if (!sync_role(p, &sh.k_sync, &syncs)) return false;
     }
-    __syncthreads();
-
-    float m_run = -INFINITY, l_run = 0.0f;
-    for (int64_t t = t_begin; t < t_end; ++t) {
-      const bool first = t == t_begin, paged = t < p.page_tiles;
-      const int64_t j0 = (t - p.page_tiles) * kTile;  // first concatenated fp16 row of an fp16 tile
-      if (tid < 5) {
-        if (tid == 4) sh.bad = 0;
-        else sh.bad_tokens[tid] = 0;
+    // fragment-order pages: the next tile's codes wait in registers and its meta words in shared memory
+    constexpr int NW = FRAG ? 4 * BK : 4;
+    uint32_t next[NW];
+    int in_tile = 0, block = 0;  // page of the tile and 32-token block of the page that this warp expands
+    auto fetch = [&](int64_t t) {
+      if constexpr (FRAG) {
+        const int64_t page = t * p.pages_per_tile + in_tile;
+        if (in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages) {
+          const uint8_t* pg = unit_pages + page * p.lay.bytes;
+          load_codes<BK>(pg + p.lay.off_kc, block, lane, next);
+          cp_async16(&sh.k_meta[t & 1][warp][4 * lane], pg + p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane);
+        }
+        cp_async_commit();
       }
-      int valid = kTile;  // columns of a page tile that hold tokens
-      if (paged) {
+    };
+    if constexpr (FRAG) {
+      in_tile = 32 * warp / p.R;
+      block = (32 * warp - in_tile * p.R) / 32;
+      fetch(w.t_begin);
+    }
+    for (int64_t t = w.t_begin; t < w.t_end; ++t, ++kt) {
+      const uint32_t st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
+      uint32_t codes[NW];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) codes[i] = next[i];
+      fetch(t + 1);
+      if (!wait(p, &sh.k_empty[st], ((kt / KS) & 1) ^ 1)) return false;
+      if (t < p.page_tiles) {
         const int64_t page0 = t * p.pages_per_tile;
-        const int64_t left = p.n_pages - page0;
-        valid = (int)(left < p.pages_per_tile ? left : p.pages_per_tile) * p.R;
         if constexpr (FRAG) {
-          // warps 0..3: keys of 32-token block `warp`, warps 4..7: values
-          const int slot = warp & 3, tok = 32 * slot;
-          if (tok < valid) {
-            const int in_tile = tok / p.R;
-            const uint8_t* pg = unit_pages + (page0 + in_tile) * p.lay.bytes;
-            const int block = (tok - in_tile * p.R) / 32;
-            if (warp < 4) key_block<BK>(p, sh, pg, block, slot, sk, lane);
-            else value_block<BV>(p, pg, block, slot, sv, lane);
-          } else if (warp < 4) {
-            for (int i = lane; i < 32 * 16; i += 32)
-              sts16(sk + tc::chunk_offset(i >> 8, tok + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
+          if (in_tile < p.pages_per_tile && page0 + in_tile < p.n_pages) {
+            cp_async_wait<1>();
+            __syncwarp();
+            key_block<BK>(codes, reinterpret_cast<const uint2*>(sh.k_meta[t & 1][warp]), sh.mu, warp, tile, lane);
           } else {
-            for (int i = lane; i < 128 * 4; i += 32)
-              sts16(sv + tc::chunk_offset(slot >> 1, i >> 2, 4 * (slot & 1) + (i & 3)), 0, 0, 0, 0);
+            for (int i = lane; i < 32 * 16; i += 32)
+              sts16(tile + tc::chunk_offset(i >> 8, 32 * warp + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
           }
           if (p.nsp > 0) {
-            __syncthreads();
-            sparse_keys(p, sh, unit_pages, page0, sk, tid);
+            if (!sync_role(p, &sh.k_sync, &syncs)) return false;
+            sparse_keys(p, sh, unit_pages, page0, tile, tid);
           }
         } else {
-          key_tile_bits<ROPE>(p, sh, unit_pages, page0, sk, warp, lane);
-          value_tile_bits(p, sh, unit_pages, page0, sv, warp, lane);
+          key_tile_bits<ROPE>(p, sh, unit_pages, page0, tile, warp, lane);
         }
       } else {
-        const int64_t end = p.n_w + x.tok0 + x.tokens;  // rows the job's last token sees
-        __syncthreads();                                // the marks are cleared
-        key_tile_f16<FRAG, ROPE>(p, sh, rows_k, new_k, j0, end, sk, warp, lane);
-        value_tile_f16(p, sh, rows_v, new_v, j0, end, p.n_w + x.tok0 + 1, sv, warp, lane);
+        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.x.tok0 + w.x.tokens, tile, warp,
+                                 lane);
       }
       fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0) {
-        tc::fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
-          tc::mma_ss(tmem, tc::descriptor(sq + off), tc::descriptor(sk + off), tc::instruction(kTile), k > 0);
+      __syncwarp();
+      if (lane == 0 && (int64_t)kt != (int64_t)p.test_withhold - 1) mbar_arrive(&sh.k_full[st]);
+    }
+    g += w.tiles();
+  }
+  return true;
+}
+
+// Value producers: warp 0..3.
+template <int BV>
+__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int64_t g_begin, int64_t g_end,
+                                           int warp, int lane) {
+  constexpr bool FRAG = BV != 0;
+  uint32_t kt = 0, jobs = 0, syncs = 0;
+  for (int64_t g = g_begin; g < g_end; ++jobs) {
+    Walk w;
+    w.at(p, g, g_end);
+    const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
+    const uint16_t* rows = p.wv + w.x.unit * p.win_unit_stride;
+    const uint16_t* fresh = p.v_new + w.x.unit * p.n * kD;
+    uint32_t* bad = sh.bad[jobs % kBadSlots];
+    if (warp == 0 && lane < 8) bad[lane] = 0;
+    if (!sync_role(p, &sh.v_sync, &syncs)) return false;
+    constexpr int NW = FRAG ? 4 * BV : 4;
+    uint32_t next[NW];
+    int in_tile = 0, block = 0;
+    const int half = p.G == 64 ? 1 : 0;
+    auto fetch = [&](int64_t t) {
+      if constexpr (FRAG) {
+        const int64_t page = t * p.pages_per_tile + in_tile;
+        if (in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages) {
+          const uint8_t* pg = unit_pages + page * p.lay.bytes;
+          load_codes<BV>(pg + p.lay.off_vc, block, lane, next);
+          if (lane < (32 >> half))
+            cp_async16(&sh.v_meta[t & 1][warp][4 * lane], pg + p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane);
         }
-        if constexpr (ROPE) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
-            tc::mma_ss(tmem, tc::descriptor(sq + off), tc::descriptor(sk + tc::kTileBytes + off),
-                       tc::instruction(kTile), true);
-          }
-        }
-        tc::commit(&sh.bar);
+        cp_async_commit();
       }
-      failed |= !mbar_wait(&sh.bar, phase);
-      phase ^= 1;
-      tc::fence_after();
-      int limit = valid;  // columns this thread's row sees
-      if (warp < 4) {
-        const int r = tid;
-        if (!paged) {
-          const int64_t seen = p.n_w + x.tok0 + (r >> p.log2hg) + 1 - j0;
-          limit = (int)(seen < 0 ? 0 : seen > kTile ? kTile : seen);
-        }
-        float mx = -INFINITY;
+    };
+    if constexpr (FRAG) {
+      in_tile = 32 * warp / p.R;
+      block = (32 * warp - in_tile * p.R) / 32;
+      fetch(w.t_begin);
+    }
+    for (int64_t t = w.t_begin; t < w.t_end; ++t, ++kt) {
+      const uint32_t st = kt % kValueStages, tile = sv + st * tc::kTileBytes;
+      uint32_t codes[NW];
 #pragma unroll
+      for (int i = 0; i < NW; ++i) codes[i] = next[i];
+      fetch(t + 1);
+      if (!wait(p, &sh.v_empty[st], ((kt / kValueStages) & 1) ^ 1)) return false;
+      if (t < p.page_tiles) {
+        const int64_t page0 = t * p.pages_per_tile;
+        if constexpr (FRAG) {
+          if (in_tile < p.pages_per_tile && page0 + in_tile < p.n_pages) {
+            cp_async_wait<1>();
+            __syncwarp();
+            value_block<BV>(codes, sh.v_meta[t & 1][warp], half, warp, tile, lane);
+          } else {
+            for (int i = lane; i < 128 * 4; i += 32)
+              sts16(tile + tc::chunk_offset(warp >> 1, i >> 2, 4 * (warp & 1) + (i & 3)), 0, 0, 0, 0);
+          }
+        } else {
+          value_tile_bits(p, sh, unit_pages, page0, tile, warp, lane);
+        }
+      } else {
+        value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.x.tok0 + w.x.tokens, p.n_w + w.x.tok0,
+                       tile, warp, lane);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.v_full[st]);
+    }
+    g += w.tiles();
+  }
+  return true;
+}
+
+// Softmax of stream q (warps 0..3 of its group, a thread per row), and the rows' results.
+template <bool FRAG>
+__device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint8_t* exchange,
+                                             uint32_t tmem, int64_t g_begin, int64_t g_end, int q, int warp, int lane) {
+  const int r = 32 * warp + lane;
+  const uint32_t my_s = tmem + 128 * q + ((uint32_t)(32 * warp) << 16), my_o = my_s + 256;
+  const int hg = 1 << p.log2hg;
+  uint32_t done = 0, jobs = 0, finals = 0, halves = 0;  // steps, pieces, pieces with steps of this stream, exchanges so far
+  for (int64_t g = g_begin; g < g_end; ++jobs) {
+    Walk w;
+    w.at(p, g, g_end);
+    const int tiles = (int)w.tiles();
+    const int64_t b = w.x.unit / p.Hkv, kvh = w.x.unit - b * p.Hkv;
+    const int64_t head_row = b * p.Hq + kvh * hg;  // query row (token i, head h): (head_row + h) * n + tok0 + i
+    // queries: job row = token * hg + head; channels in the key tiles' column order.  This stream's last
+    // product of the piece before has finished, and with it every earlier one that read the tile.
+    {
+      const int first = w.dual ? 64 * q : 128 * q, count = w.dual ? 64 : 128;
+      for (int task = warp; task < count / 8; task += 4) {
+        const int row = first + 8 * task + (lane >> 2), c = lane & 3;
+        uint4 v[4] = {};
+        if (row < w.rows) {
+          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.x.tok0 + (row >> p.log2hg);
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + src_row * kD) + 4 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
+        }
+        const uint32_t tile = sq + (row >> 7) * tc::kTileBytes;
+        if constexpr (FRAG) {
+          store_frag_row(tile, row & 127, c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts16(tile + tc::chunk_offset(c >> 1, row & 127, 4 * (c & 1) + i), v[i].x, v[i].y, v[i].z, v[i].w);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&sh.q_full[q]);
+
+    const int job_row = w.dual ? r : 128 * q + r;
+    const int64_t seen0 = p.n_w + w.x.tok0 + (job_row >> p.log2hg) + 1;  // fp16 rows this row sees
+    const bool live = job_row - lane < w.rows;
+    float m_run = -INFINITY, l_run = 0.0f;
+    const int steps = w.dual ? (tiles - q + 1) / 2 : tiles;
+    for (int i = 0; i < steps; ++i, ++done) {
+      const int64_t t = w.t_begin + (w.dual ? 2 * i + q : i);
+      int limit;  // columns this row sees
+      if (t < p.page_tiles) {
+        const int64_t left = p.n_pages - t * p.pages_per_tile;
+        limit = (int)(left < p.pages_per_tile ? left : p.pages_per_tile) * p.R;
+      } else {
+        const int64_t seen = seen0 - (t - p.page_tiles) * kTile;
+        limit = (int)(seen < 0 ? 0 : seen > kTile ? kTile : seen);
+      }
+      if (!wait(p, &sh.s_full[q], done & 1)) return false;
+      tc::fence_after();
+      if (!live) {  // no query row in this warp: its rows of S, P and O are never looked at
+        tc::fence_before();
+        mbar_arrive(&sh.p_ready[q]);
+        continue;
+      }
+      if (__any_sync(0xffffffffu, limit < kTile)) {  // hidden columns to -inf, whatever they hold
+#pragma unroll 1
         for (int y = 0; y < 4; ++y) {
           uint32_t s[32];
-          tc::ld32(my_tmem + 32 * y, s);
+          tc::ld32(my_s + 32 * y, s);
           tc::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * y + i < limit) mx = fmaxf(mx, __uint_as_float(s[i]));
-        }
-        const float ms = mx * p.scale_log2;
-        const bool renew = ms > m_run + kLazy;  // also from -inf
-        const float factor = renew ? ex2(m_run - ms) : 1.0f;
-        if (renew) m_run = ms;
-        l_run *= factor;
-        if (!first && __any_sync(0xffffffffu, renew)) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t o[32];
-            tc::ld32(my_tmem + kTile + 32 * y, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-            tc::st32(my_tmem + kTile + 32 * y, o);
-          }
-        }
-        const float shift = kWeightExp - (m_run == -INFINITY ? 0.0f : m_run);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t s[32], w[16];
-          tc::ld32(my_tmem + 32 * y, s);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float a = ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, shift));
-            float c = ex2(fmaf(__uint_as_float(s[i + 1]), p.scale_log2, shift));
-            a = 32 * y + i < limit ? a : 0.0f;
-            c = 32 * y + i + 1 < limit ? c : 0.0f;
-            l_run += a + c;
-            w[i / 2] = u32(__floats2half2_rn(a, c));
-          }
-          tc::st16(my_tmem + 16 * y, w);
+          for (int k = 0; k < 32; ++k) s[k] = 32 * y + k < limit ? s[k] : 0xFF800000u;
+          tc::st32(my_s + 32 * y, s);
         }
         tc::wait_st();
       }
-      tc::fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc::fence_after();
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int y = 0; y < 4; ++y) {
+        uint32_t s[32];
+        tc::ld32(my_s + 32 * y, s);
+        tc::wait_ld();
+        float m1 = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
-          tc::mma_ts(tmem + kTile, tmem + 8 * k, tc::descriptor(sv + off), tc::instruction(kD), !(first && k == 0));
+        for (int k = 0; k < 32; k += 4) {
+          mx = max3(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+          m1 = max3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
         }
-        tc::commit(&sh.bar);
+        mx = fmaxf(mx, m1);
       }
-      failed |= !mbar_wait(&sh.bar, phase);
-      phase ^= 1;
+      const float ms = mx * p.scale_log2;
+      const bool renew = ms > m_run + kLazy;  // also from -inf
+      const float factor = renew ? ex2(m_run - ms) : 1.0f;
+      if (renew) m_run = ms;
+      l_run *= factor;
+      // the stream's product before finished with the S that was just read (they were committed together)
+      if (i > 0 && __any_sync(0xffffffffu, renew)) {
+#pragma unroll 1
+        for (int y = 0; y < 4; ++y) {
+          uint32_t o[32];
+          tc::ld32(my_o + 32 * y, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
+          tc::st32(my_o + 32 * y, o);
+        }
+      }
+      const float shift = kWeightExp - (m_run == -INFINITY ? 0.0f : m_run);
+      const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(shift, shift);
+      uint64_t sum2 = 0;
+#pragma unroll 1
+      for (int y = 0; y < 4; ++y) {
+        uint32_t s[32], wt[16];
+        tc::ld32(my_s + 32 * y, s);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float a, c;
+          unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, shift2), a, c);
+          a = ex2(a);
+          c = ex2(c);
+          sum2 = add2(sum2, pack2(a, c));
+          wt[k / 2] = u32(__floats2half2_rn(a, c));
+        }
+        tc::st16(my_s + 16 * y, wt);
+      }
+      float la, lb;
+      unpack2(sum2, la, lb);
+      l_run += la + lb;
+      tc::wait_st();
+      tc::fence_before();
+      mbar_arrive(&sh.p_ready[q]);
+    }
+    if (steps > 0) {
+      if (!wait(p, &sh.o_done[q], finals & 1)) return false;
+      ++finals;
       tc::fence_after();
-      if (warp < 4 && sh.bad) patch_values(p, sh, rows_v, new_v, j0, limit, my_tmem);
-      failed = __syncthreads_or(failed);
-      if (failed) break;
+    } else if (!wait(p, &sh.o_done[0], jobs & 1)) {  // a stream without steps must not run ahead into the next queries
+      return false;
     }
 
-    // the row's result, or its partial when the job is cut
-    if (warp < 4 && !failed) {
-      const bool whole = t_begin == 0 && t_end == x.tiles;
-      const int r = tid;
-      const float inv = l_run > 0.0f ? 1.0f / l_run : l_run == 0.0f ? 0.0f : l_run;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (t_begin == 0 ? 1 : 0);
-      const int64_t row = (b * p.Hq + kvh * hg + (r & (hg - 1))) * p.n + x.tok0 + (r >> p.log2hg);
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
+    // the row's result, or its partial when the job is cut; two streams of the same rows are joined first
+    const bool whole = w.t_begin == 0 && w.t_end == w.x.tiles;
+    const bool join = w.dual && tiles > 1;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (w.t_begin == 0 ? 1 : 0);
+    float* xo = reinterpret_cast<float*>(exchange);  // [64 columns][128 rows]
+    float f0 = 1.0f, f1 = 0.0f;
+    const uint32_t* bad = sh.bad[jobs % kBadSlots];
+    const bool patch = whole || w.t_end > p.page_tiles
+                           ? (bad[0] | bad[1] | bad[2] | bad[3] | bad[4] | bad[5] | bad[6] | bad[7]) != 0
+                           : false;
+#pragma unroll 1
+    for (int y = 0; y < 4; ++y) {
+      if (join && q == 1) {
         uint32_t o[32];
-        tc::ld32(my_tmem + kTile + 32 * y, o);
+        tc::ld32(my_o + 32 * y, o);
         tc::wait_ld();
-        if (r < rows) {
-          // column 8c + (e << 2 | i) holds channel 8c + 2i + e
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD) + 4 * y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = u32(__floats2half2_rn(__uint_as_float(o[8 * c + i]) * inv, __uint_as_float(o[8 * c + 4 + i]) * inv));
-              dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_acc + (slot * p.rows_max + r) * kD) + 8 * y;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; i += 2)
-                dst[2 * c + i / 2] = make_float4(__uint_as_float(o[8 * c + i]), __uint_as_float(o[8 * c + 4 + i]),
-                                                 __uint_as_float(o[8 * c + i + 1]), __uint_as_float(o[8 * c + 5 + i]));
-          }
+        for (int k = 0; k < 32; ++k) xo[(32 * (y & 1) + k) * kRows + r] = __uint_as_float(o[k]);
+        if (y == 0) {
+          sh.xm[r] = m_run;
+          sh.xl[r] = l_run;
+        }
+        if (y & 1) {
+          mbar_arrive(&sh.x_written);
+          if (!wait(p, &sh.x_read, halves++ & 1)) return false;
+        }
+        continue;
+      }
+      if (w.dual && q == 1) break;
+      if (join && !(y & 1)) {
+        if (y) mbar_arrive(&sh.x_read);
+        if (!wait(p, &sh.x_written, halves++ & 1)) return false;
+        if (y == 0) {
+          const float m1 = sh.xm[r], m = fmaxf(m_run, m1);
+          f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m);
+          f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
+          l_run = l_run * f0 + sh.xl[r] * f1;
+          m_run = m;
         }
       }
-      if (!whole && r < rows)
-        *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows_max + r) * 2) = make_float2(m_run, l_run);
+      uint32_t o[32];
+      tc::ld32(my_o + 32 * y, o);
+      tc::wait_ld();
+      if (join) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + xo[(32 * (y & 1) + k) * kRows + r] * f1);
+      }
+      if (patch) {
+        uint32_t fixed[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) fixed[k] = o[k];
+        patch_values(bad, p.v_new + (w.x.unit * p.n + w.x.tok0) * kD, min(job_row >> p.log2hg, w.x.tokens - 1), y, fixed);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = fixed[k];
+      }
+      if (job_row < w.rows) {
+        // column 8c + (e << 2 | i) holds channel 8c + 2i + e
+        if (whole) {
+          const float inv = l_run > 0.0f ? 1.0f / l_run : l_run == 0.0f ? 0.0f : l_run;
+          const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + w.x.tok0 + (job_row >> p.log2hg);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD) + 4 * y;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = u32(__floats2half2_rn(__uint_as_float(o[8 * c + k]) * inv, __uint_as_float(o[8 * c + 4 + k]) * inv));
+            dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_acc + (slot * p.rows_max + job_row) * kD) + 8 * y;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2)
+              dst[2 * c + k / 2] = make_float4(__uint_as_float(o[8 * c + k]), __uint_as_float(o[8 * c + 4 + k]),
+                                               __uint_as_float(o[8 * c + k + 1]), __uint_as_float(o[8 * c + 5 + k]));
+          if (y == 0)
+            *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows_max + job_row) * 2) = make_float2(m_run, l_run);
+        }
+      }
     }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    g += t_end - t_begin;
+    if (join && q == 0) mbar_arrive(&sh.x_read);
+    tc::fence_before();  // O is read before the next piece's first product, which waits for its queries
+    g += tiles;
   }
-  if (failed && tid == 0) report_error(p.err, kDevWaitTimeout);
+  return true;
+}
+
+// BK, BV: code widths of fragment-order pages, or 0 for bitstream pages (widths at run time).
+template <int BK, int BV, bool ROPE>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared sh;
+  uint8_t* const base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t sq = smem_u32(base), sk = sq + 2 * tc::kTileBytes;
+  const uint32_t sv = sk + kKeyStages<ROPE> * kKeyBytes<ROPE>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kIssuer = 8 + 2 * kProducers;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], kProducers);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], kProducers);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], kRows);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.q_full[i], kRows);
+    }
+    mbar_init(&sh.x_written, kRows);
+    mbar_init(&sh.x_read, kRows);
+    mbar_init(&sh.k_sync, kProducers * 32);
+    mbar_init(&sh.v_sync, kProducers * 32);
+    fence_mbar_init();
+  }
+  if (tid < 16) {
+    sh.k_lev[tid] = p.k_lev[tid];
+    sh.v_lev[tid] = p.v_lev[tid];
+  }
+  if (warp == kIssuer) tc::alloc(&sh.tmem, kTmemColumns);
+  tc::fence_before();
   __syncthreads();
-  if (warp == 0) tc::dealloc(tmem, kTmemColumns);
+  tc::fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_allow_next();
+
+  const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
+  const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
+  bool ok = true;
+  if (warp < 8) {
+    ok = softmax_role<BK != 0>(p, sh, sq, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
+  } else if (warp < 8 + kProducers) {
+    ok = key_role<BK, ROPE>(p, sh, sk, g_begin, g_end, warp - 8, lane);
+  } else if (warp < kIssuer) {
+    ok = value_role<BV>(p, sh, sv, g_begin, g_end, warp - 8 - kProducers, lane);
+  } else if (lane == 0) {
+    ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, g_begin, g_end);
+  }
+  if (!ok) report_error(p.err, kDevWaitTimeout);
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kIssuer) tc::dealloc(tmem, kTmemColumns);
 }
 
 // Join the partials of the jobs that the cuts between CTAs divide: CTA x of the grid handles the job that
@@ -799,13 +1138,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid
   }
 }
 
-constexpr int kCtasPerSm = 2;
-
-int64_t slot_rows(int64_t n, int hg) { return n * hg < kRows ? n * hg : kRows; }
+// Rows of a partial slot: a job's.
+int64_t slot_rows(int64_t n, int hg) { return n >= 2 * kRows / hg ? 2 * kRows : n * hg; }
 
 template <int BK, int BV, bool ROPE>
 cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStream_t s) {
-  constexpr size_t smem = (ROPE ? 4 : 3) * tc::kTileBytes + 1024;
+  constexpr size_t smem = kSmemBytes<ROPE>;
   cudaError_t e = cudaFuncSetAttribute(chunk_kernel<BK, BV, ROPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   chunk_kernel<BK, BV, ROPE><<<(unsigned)grid, kThreads, smem, s>>>(p);
@@ -832,12 +1170,12 @@ cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStre
 
 // Two partial slots per CTA, each with the rows a job can have, of D + 2 floats a row.
 int64_t chunk_workspace_bytes(int64_t n, int hg, int sm_count) {
-  return 2 * (int64_t)kCtasPerSm * sm_count * slot_rows(n, hg) * (kD + 2) * (int64_t)sizeof(float);
+  return 2 * (int64_t)sm_count * slot_rows(n, hg) * (kD + 2) * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace, int* launches, cudaStream_t s) {
   const int hg = 1 << p.log2hg;
-  p.log2_job_tokens = 7 - p.log2hg;
+  p.log2_job_tokens = (p.n * hg > kRows ? 8 : 7) - p.log2hg;
   p.pages_per_tile = kTile / p.R;
   p.page_tiles = (p.n_pages + p.pages_per_tile - 1) / p.pages_per_tile;
   const int64_t job_tokens = (int64_t)1 << p.log2_job_tokens;
@@ -845,13 +1183,12 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   p.tiles_per_unit = p.jobs_per_unit * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, p.jobs_per_unit - 1) +
                      ((p.n_w + p.n + 127) >> 7);
   p.total_tiles = p.n_units * p.tiles_per_unit;
-  const int64_t resident = (int64_t)(rope ? 1 : kCtasPerSm) * sm_count;
-  int64_t grid = p.total_tiles < resident ? p.total_tiles : resident;
+  int64_t grid = p.total_tiles < sm_count ? p.total_tiles : sm_count;
   p.per_cta = (p.total_tiles + grid - 1) / grid;
   grid = (p.total_tiles + p.per_cta - 1) / p.per_cta;
   p.rows_max = (int32_t)slot_rows(p.n, hg);
   p.part_acc = static_cast<float*>(workspace);
-  p.part_ml = p.part_acc + 2 * resident * p.rows_max * kD;
+  p.part_ml = p.part_acc + 2 * (int64_t)sm_count * p.rows_max * kD;
   if (p.lay.frag) {
     if (p.bk == 2 && p.bv == 2) return launch_t<2, 2, false>(p, grid, launches, s);
     if (p.bk == 4 && p.bv == 2) return launch_t<4, 2, false>(p, grid, launches, s);

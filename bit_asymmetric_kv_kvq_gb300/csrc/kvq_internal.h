@@ -169,7 +169,7 @@ struct CopySequencesParams {
   int* err;
 };
 
-// Attention of a chunk of new tokens (kvq_chunk.cu).  The work list is cut into jobs -- 128 query
+// Attention of a chunk of new tokens (kvq_chunk.cu).  The work list is cut into jobs -- up to 256 query
 // rows (token-major, the heads of a kv head beside each other) of one unit -- and a job into tiles
 // of up to 128 keys: the page tiles, then tiles over the unit's fp16 rows followed by the new tokens.
 struct ChunkParams {
@@ -190,6 +190,8 @@ struct ChunkParams {
   int* err;
   int32_t lut;
   float k_lev[16], v_lev[16];
+  unsigned long long wait_ns;  // test hooks, as in DecodeParams: withhold tile k of every CTA's piece of the list
+  int32_t test_withhold;
   int32_t pages_per_tile;   // the rest is set by the launcher
   int64_t page_tiles;       // page tiles of a unit
   int64_t jobs_per_unit, tiles_per_unit, total_tiles, per_cta;
