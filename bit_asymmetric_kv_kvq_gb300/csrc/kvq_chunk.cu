@@ -51,9 +51,16 @@ constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O a
 constexpr int kValueStages = 2;
 constexpr int kBadSlots = 4;       // marks of non-finite values: producers run at most three jobs ahead
 
+// A place in the work list: a job, and where its tiles begin.
+struct Piece {
+  int64_t unit, job;         // job of the unit
+  int64_t job_start;         // its first tile in the flat list
+};
+
 struct __align__(16) Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_ready[2], o_done[2], q_full[2], x_written, x_read, k_sync, v_sync;
+  Piece first;                 // where this CTA's part of the work list begins
   uint32_t tmem;
   uint32_t bad[kBadSlots][8];  // tokens of the job with a non-finite value that some of its rows must not see
   __half2 mu[kD / 2];          // per channel pair
@@ -84,15 +91,7 @@ __host__ __device__ inline int64_t f16_tiles_before(int64_t n_w, int log2_job_to
   return sum;
 }
 
-struct Piece {
-  int64_t unit, job;         // job of the unit
-  int64_t job_start;         // its first tile in the flat list
-  int64_t tiles;             // its tiles
-  int64_t tok0;              // first chunk token of the job
-  int tokens;                // chunk tokens of the job
-};
-
-__host__ __device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t g) {
+__device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t g) {
   Piece x;
   x.unit = g / p.tiles_per_unit;
   const int64_t r = g - x.unit * p.tiles_per_unit;
@@ -104,11 +103,17 @@ __host__ __device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t 
   }
   x.job = lo;
   x.job_start = x.unit * p.tiles_per_unit + lo * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, lo);
-  x.tok0 = lo << p.log2_job_tokens;
-  const int64_t left = p.n - x.tok0, full = (int64_t)1 << p.log2_job_tokens;
-  x.tokens = (int)(left < full ? left : full);
-  x.tiles = p.page_tiles + ((p.n_w + x.tok0 + x.tokens + 127) >> 7);
   return x;
+}
+
+// The job at a place: its first chunk token, its tokens and its tiles.
+__device__ __forceinline__ int64_t job_tok0(const ChunkParams& p, const Piece& x) { return x.job << p.log2_job_tokens; }
+__device__ __forceinline__ int job_tokens(const ChunkParams& p, const Piece& x) {
+  const int64_t left = p.n - job_tok0(p, x), full = (int64_t)1 << p.log2_job_tokens;
+  return (int)(left < full ? left : full);
+}
+__device__ __forceinline__ int64_t job_tiles(const ChunkParams& p, const Piece& x) {
+  return p.page_tiles + ((p.n_w + job_tok0(p, x) + job_tokens(p, x) + 127) >> 7);
 }
 
 // ------------------------------------------------------------ operand tiles
@@ -514,9 +519,11 @@ __device__ __forceinline__ void value_tile_f16(const ChunkParams& p, uint32_t* b
 
 // What the marked tokens up to the row's own add to its channels 32y .. 32y + 31: their non-finite values
 // (every visible token has a positive weight, so inf or NaN is the sum's).  `o` is in value_row order.
-__device__ __noinline__ void patch_values(const uint32_t* bad, const uint16_t* job_v, int token, int y, uint32_t* o) {
+__device__ __forceinline__ void patch_values(const uint32_t* bad, const uint16_t* job_v, int token, int y, uint32_t* o) {
+#pragma unroll 1
   for (int i = 1; i <= token; ++i) {
     if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
+#pragma unroll 1
     for (int c = 0; c < 32; ++c) {
       const float f = __half2float(__ushort_as_half(job_v[(int64_t)i * kD + 32 * y + c]));
       if (!isfinite(f)) o[value_row(c)] = __float_as_uint(__uint_as_float(o[value_row(c)]) + f);
@@ -568,25 +575,43 @@ constexpr int kSmemBytes = 2 * tc::kTileBytes + kKeyStages<ROPE> * kKeyBytes<ROP
 // A CTA's walk over its pieces of the work list: what every role needs to know of one.
 struct Walk {
   Piece x;
-  int64_t t_begin, t_end;  // tiles of the job in this piece
-  bool dual;               // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
-  int rows;
+  int64_t tok0, job_tiles_;  // first chunk token of the job, its tiles
+  int64_t t_begin, t_end;    // tiles of the job in this piece
+  int tokens, rows;          // chunk tokens and query rows of the job
+  bool dual;                 // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
+  __device__ __forceinline__ explicit Walk(const Piece& first) : x(first) {}
   __device__ __forceinline__ void at(const ChunkParams& p, int64_t g, int64_t g_end) {
-    x = find_piece(p, g);
+    tok0 = job_tok0(p, x);
+    tokens = job_tokens(p, x);
+    job_tiles_ = job_tiles(p, x);
     t_begin = g - x.job_start;
     const int64_t left = t_begin + (g_end - g);
-    t_end = x.tiles < left ? x.tiles : left;
-    rows = x.tokens << p.log2hg;
+    t_end = job_tiles_ < left ? job_tiles_ : left;
+    rows = tokens << p.log2hg;
     dual = rows <= kRows;
   }
   __device__ __forceinline__ int64_t tiles() const { return t_end - t_begin; }
+  __device__ __forceinline__ void next(const ChunkParams& p) {  // the job behind (used when a piece ends its job)
+    x.job_start += job_tiles_;
+    if (++x.job == p.jobs_per_unit) {
+      x.job = 0;
+      ++x.unit;
+    }
+  }
 };
 
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit) {
-  return mbar_wait(bar, parity, limit ? limit : kWaitLimitNs);
-}
+// Waits poll with the barrier's own short suspension and look at the clock every 256 polls.
 __device__ __forceinline__ bool wait(const ChunkParams& p, uint64_t* bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, p.wait_ns);
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) == 0) {
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > (p.wait_ns ? p.wait_ns : kWaitLimitNs)) return false;
+    }
+  }
+  return true;
 }
 
 // Barrier among the warps of one role, with the time limit of every wait (a hardware barrier has none).
@@ -595,64 +620,85 @@ __device__ __forceinline__ bool sync_role(const ChunkParams& p, uint64_t* bar, u
   return wait(p, bar, (*count)++ & 1);
 }
 
-// One product of a stream with a tile: S = Q K^T (hi and lo halves of rotated keys), or O (+)= P V.
+// The value of lane 0, known to be the same in every lane.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// One product of a stream with a tile: S = Q K^T (hi and lo halves of rotated keys), or O (+)= P V.  A
+// descriptor's high word is the same for every tile; the low word moves by 2 (32 bytes) with every 16
+// columns and by a block's size after 64.
 template <bool ROPE>
-__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sq, uint32_t sk) {
+__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k) {
 #pragma unroll
   for (int h = 0; h < (ROPE ? 2 : 1); ++h)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
-      tc::mma_ss(d, tc::descriptor(sq + off), tc::descriptor(sk + h * tc::kTileBytes + off), tc::instruction(kTile),
-                 h > 0 || k > 0);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t off = ((i >> 2) * tc::kBlockBytes + (i & 3) * 32) >> 4;
+      tc::mma_ss(d, q + off, k + (h * (tc::kTileBytes >> 4) + off), tc::instruction(kTile), h > 0 || i > 0);
     }
 }
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint32_t sv, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint64_t v, bool accumulate) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t off = (k >> 2) * tc::kBlockBytes + (k & 3) * 32;
-    tc::mma_ts(d, pcol + 8 * k, tc::descriptor(sv + off), tc::instruction(kD), accumulate || k > 0);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t off = ((i >> 2) * tc::kBlockBytes + (i & 3) * 32) >> 4;
+    tc::mma_ts(d, pcol + 8 * i, v + off, tc::instruction(kD), accumulate || i > 0);
   }
 }
 
-// The issuing thread.  Step s of a piece is one stream's turn at one tile; QK runs two steps ahead of PV, so
+// The issuing warp.  Step s of a piece is one stream's turn at one tile; QK runs two steps ahead of PV, so
 // between a stream's QK and its PV the tensor cores have the other stream's products.  P overlies S: QK of
-// step s + 2 comes behind PV of step s, which reads P, in issue order.
+// step s + 2 comes behind PV of step s, which reads P, in issue order.  The warp walks along as a whole
+// with everything uniform, so addresses and descriptors stay in uniform registers, and waits for one
+// barrier a step: the tensor cores hold only a few products in advance, so what lies between two steps'
+// products is their idle time.  The softmax streams watch the operand tiles for it (see operands_ready).
 template <bool ROPE>
 __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sk, uint32_t sv,
-                                           uint32_t tmem, int64_t g_begin, int64_t g_end) {
+                                           uint32_t tmem_, int64_t g_begin, int64_t g_end) {
   constexpr int KS = kKeyStages<ROPE>;
-  uint32_t kt0 = 0, jobs = 0, used[2] = {0, 0};  // tiles and pieces so far, steps of each stream so far
-  for (int64_t g = g_begin; g < g_end; ++jobs) {
-    Walk w;
+  const bool leader = tc::elect();
+  const uint32_t tmem = uniform(tmem_);
+  const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv);
+  uint32_t kt = 0, vt = 0, jobs = 0, used0 = 0, used1 = 0;  // key and value tiles, pieces, steps of the streams so far
+  Walk w(sh.first);
+  bool more = g_begin < g_end;
+  for (int64_t g = g_begin; uniform(more); w.next(p)) {
     w.at(p, g, g_end);
-    const int tiles = (int)w.tiles(), steps = w.dual ? tiles : 2 * tiles;
+    const bool dual = uniform(w.dual);
+    const int tiles = (int)uniform((uint32_t)w.tiles()), steps = dual ? tiles : 2 * tiles;
     if (!wait(p, &sh.q_full[0], jobs & 1) || !wait(p, &sh.q_full[1], jobs & 1)) return false;
+    ++jobs;
 #pragma unroll 1
     for (int s = -2; s < steps; ++s) {
-      const int q = s & 1;
-      const uint32_t at = 128 * q, kt = kt0 + (w.dual ? s : s >> 1);  // of step s; QK's tile is one or two on
-      if (s >= 0) {
-        const uint32_t st = kt % kValueStages;
-        if (!wait(p, &sh.v_full[st], (kt / kValueStages) & 1)) return false;
-        if (!wait(p, &sh.p_ready[q], used[q] & 1)) return false;
-        used[q]++;
-        tc::fence_after();
-        issue_pv(tmem + 256 + at, tmem + at, sv + st * tc::kTileBytes, s >= 2);
-        if (w.dual || q == 1) tc::commit(&sh.v_empty[st]);
-        if (s + 2 >= steps) tc::commit(&sh.o_done[q]);
+      const uint32_t q = s & 1, at = 128 * q;
+      const bool last = dual || q == 1;  // the tile's last step
+      const uint32_t vs = vt % kValueStages, ks = kt % KS;
+      if (s >= 0) {  // the stream's weights, its value tile and the key tile of its next step are there
+        if (!wait(p, &sh.p_ready[q], (q ? used1 : used0) & 1)) return false;
+        if (q) ++used1;
+        else ++used0;
+      } else if (s + 2 < steps) {
+        if (!wait(p, &sh.k_full[ks], (kt / KS) & 1)) return false;
       }
-      if (s + 2 < steps) {
-        const uint32_t kn = kt + (w.dual ? 2 : 1), st = kn % KS;
-        if (!wait(p, &sh.k_full[st], (kn / KS) & 1)) return false;
-        tc::fence_after();
-        issue_qk<ROPE>(tmem + at, sq + (w.dual ? 0 : q * tc::kTileBytes), sk + st * kKeyBytes<ROPE>);
-        tc::commit(&sh.s_full[q]);
-        if (w.dual || q == 1) tc::commit(&sh.k_empty[st]);
+      tc::fence_after();
+      if (leader) {
+        if (s >= 0) {
+          issue_pv(tmem + 256 + at, tmem + at, dv + vs * (tc::kTileBytes >> 4), s >= 2);
+          if (last) tc::commit(&sh.v_empty[vs]);
+        }
+        if (s + 2 < steps) {
+          issue_qk<ROPE>(tmem + at, dq + (dual ? 0 : q * (tc::kTileBytes >> 4)), dk + ks * (kKeyBytes<ROPE> >> 4));
+          tc::commit(&sh.s_full[q]);
+        } else if (s >= 0) {
+          tc::commit(&sh.o_done[q]);
+        }
+      }
+      __syncwarp();
+      if (last) {
+        vt += s >= 0 ? 1 : 0;
+        kt += s + 2 < steps ? 1 : 0;
       }
     }
-    kt0 += tiles;
     g += tiles;
+    more = g < g_end;
   }
   return true;
 }
@@ -665,8 +711,8 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
   constexpr int KS = kKeyStages<ROPE>;
   const int tid = 32 * warp + lane;
   uint32_t kt = 0, syncs = 0;
-  for (int64_t g = g_begin; g < g_end;) {
-    Walk w;
+  Walk w(sh.first);
+  for (int64_t g = g_begin; g < g_end; w.next(p)) {
     w.at(p, g, g_end);
     const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
     const uint16_t* rows = p.wk + w.x.unit * p.win_unit_stride;
@@ -730,7 +776,7 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
           key_tile_bits<ROPE>(p, sh, unit_pages, page0, tile, warp, lane);
         }
       } else {
-        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.x.tok0 + w.x.tokens, tile, warp,
+        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, tile, warp,
                                  lane);
       }
       fence_proxy_async_smem();
@@ -748,8 +794,8 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
-  for (int64_t g = g_begin; g < g_end; ++jobs) {
-    Walk w;
+  Walk w(sh.first);
+  for (int64_t g = g_begin; g < g_end; ++jobs, w.next(p)) {
     w.at(p, g, g_end);
     const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
     const uint16_t* rows = p.wv + w.x.unit * p.win_unit_stride;
@@ -800,7 +846,7 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
           value_tile_bits(p, sh, unit_pages, page0, tile, warp, lane);
         }
       } else {
-        value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.x.tok0 + w.x.tokens, p.n_w + w.x.tok0,
+        value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, p.n_w + w.tok0,
                        tile, warp, lane);
       }
       fence_proxy_async_smem();
@@ -813,15 +859,25 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
 }
 
 // Softmax of stream q (warps 0..3 of its group, a thread per row), and the rows' results.
-template <bool FRAG>
+// What a step's products need besides the weights: its value tile, and the key tile of the stream's next step
+// (`ahead` tiles on, if the piece has it).  One thread of the stream waits before it reports its weights.
+template <int KS>
+__device__ __forceinline__ bool operands_ready(const ChunkParams& p, Shared& sh, uint32_t tile, uint32_t ahead,
+                                               uint32_t end) {
+  if (!wait(p, &sh.v_full[tile % kValueStages], (tile / kValueStages) & 1)) return false;
+  const uint32_t next = tile + ahead;
+  return next >= end || wait(p, &sh.k_full[next % KS], (next / KS) & 1);
+}
+
+template <bool FRAG, int KS>
 __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint8_t* exchange,
                                              uint32_t tmem, int64_t g_begin, int64_t g_end, int q, int warp, int lane) {
   const int r = 32 * warp + lane;
   const uint32_t my_s = tmem + 128 * q + ((uint32_t)(32 * warp) << 16), my_o = my_s + 256;
   const int hg = 1 << p.log2hg;
-  uint32_t done = 0, jobs = 0, finals = 0, halves = 0;  // steps, pieces, pieces with steps of this stream, exchanges so far
-  for (int64_t g = g_begin; g < g_end; ++jobs) {
-    Walk w;
+  uint32_t tiles0 = 0, done = 0, jobs = 0, finals = 0, halves = 0;  // tiles, steps, pieces, pieces with steps of this stream, exchanges so far
+  Walk w(sh.first);
+  for (int64_t g = g_begin; g < g_end; ++jobs, w.next(p)) {
     w.at(p, g, g_end);
     const int tiles = (int)w.tiles();
     const int64_t b = w.x.unit / p.Hkv, kvh = w.x.unit - b * p.Hkv;
@@ -834,7 +890,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         const int row = first + 8 * task + (lane >> 2), c = lane & 3;
         uint4 v[4] = {};
         if (row < w.rows) {
-          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.x.tok0 + (row >> p.log2hg);
+          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.tok0 + (row >> p.log2hg);
           const uint4* src = reinterpret_cast<const uint4*>(p.q + src_row * kD) + 4 * c;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
@@ -853,9 +909,10 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     mbar_arrive(&sh.q_full[q]);
 
     const int job_row = w.dual ? r : 128 * q + r;
-    const int64_t seen0 = p.n_w + w.x.tok0 + (job_row >> p.log2hg) + 1;  // fp16 rows this row sees
+    const int64_t seen0 = p.n_w + w.tok0 + (job_row >> p.log2hg) + 1;  // fp16 rows this row sees
     const bool live = job_row - lane < w.rows;
-    float m_run = -INFINITY, l_run = 0.0f;
+    float m_run = -INFINITY;
+    uint64_t sum2 = 0;  // l in two halves
     const int steps = w.dual ? (tiles - q + 1) / 2 : tiles;
     for (int i = 0; i < steps; ++i, ++done) {
       const int64_t t = w.t_begin + (w.dual ? 2 * i + q : i);
@@ -869,78 +926,80 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
       }
       if (!wait(p, &sh.s_full[q], done & 1)) return false;
       tc::fence_after();
+      const uint32_t tile = tiles0 + (w.dual ? 2 * i + q : i);  // of all tiles of this CTA
+      if (r == kRows - 32 && (w.dual || q == 1)) mbar_arrive(&sh.k_empty[tile % KS]);  // its last product is done
       if (!live) {  // no query row in this warp: its rows of S, P and O are never looked at
         tc::fence_before();
+        if (r == kRows - 32 && !operands_ready<KS>(p, sh, tile, w.dual ? 2 : 1, tiles0 + tiles)) return false;
         mbar_arrive(&sh.p_ready[q]);
         continue;
       }
-      if (__any_sync(0xffffffffu, limit < kTile)) {  // hidden columns to -inf, whatever they hold
-#pragma unroll 1
-        for (int y = 0; y < 4; ++y) {
-          uint32_t s[32];
-          tc::ld32(my_s + 32 * y, s);
-          tc::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) s[k] = 32 * y + k < limit ? s[k] : 0xFF800000u;
-          tc::st32(my_s + 32 * y, s);
-        }
-        tc::wait_st();
-      }
+      const bool masked = __any_sync(0xffffffffu, limit < kTile);
       float mx = -INFINITY;
 #pragma unroll 1
-      for (int y = 0; y < 4; ++y) {
-        uint32_t s[32];
-        tc::ld32(my_s + 32 * y, s);
+      for (int col = 0; col < kTile; col += 32) {
+        uint32_t v[32];
+        tc::ld32(my_s + col, v);
         tc::wait_ld();
+        tc::tie32(v);
+        if (masked) {  // hidden columns to -inf, whatever they hold
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = col + k < limit ? v[k] : 0xFF800000u;
+          tc::st32(my_s + col, v);
+        }
         float m1 = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
-          mx = max3(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-          m1 = max3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+          mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
         }
         mx = fmaxf(mx, m1);
       }
+      if (masked) tc::wait_st();
       const float ms = mx * p.scale_log2;
       const bool renew = ms > m_run + kLazy;  // also from -inf
-      const float factor = renew ? ex2(m_run - ms) : 1.0f;
-      if (renew) m_run = ms;
-      l_run *= factor;
-      // the stream's product before finished with the S that was just read (they were committed together)
-      if (i > 0 && __any_sync(0xffffffffu, renew)) {
+      if (__any_sync(0xffffffffu, renew)) {
+        const float factor = renew ? ex2(m_run - ms) : 1.0f;
+        if (renew) m_run = ms;
+        float lo, hi;
+        unpack2(sum2, lo, hi);
+        sum2 = pack2(lo * factor, hi * factor);
+        // the stream's product before finished with the S that was just read (they were committed together)
+        if (i > 0) {
 #pragma unroll 1
-        for (int y = 0; y < 4; ++y) {
-          uint32_t o[32];
-          tc::ld32(my_o + 32 * y, o);
-          tc::wait_ld();
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t o[32];
+            tc::ld32(my_o + c, o);
+            tc::wait_ld();
+            tc::tie32(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
-          tc::st32(my_o + 32 * y, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
+            tc::st32(my_o + c, o);
+          }
         }
       }
       const float shift = kWeightExp - (m_run == -INFINITY ? 0.0f : m_run);
       const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(shift, shift);
-      uint64_t sum2 = 0;
 #pragma unroll 1
-      for (int y = 0; y < 4; ++y) {
-        uint32_t s[32], wt[16];
-        tc::ld32(my_s + 32 * y, s);
+      for (int col = 0; col < kTile; col += 32) {
+        uint32_t v[32], wt[16];
+        tc::ld32(my_s + col, v);
         tc::wait_ld();
+        tc::tie32(v);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           float a, c;
-          unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, shift2), a, c);
+          unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2, shift2), a, c);
           a = ex2(a);
           c = ex2(c);
           sum2 = add2(sum2, pack2(a, c));
           wt[k / 2] = u32(__floats2half2_rn(a, c));
         }
-        tc::st16(my_s + 16 * y, wt);
+        tc::st16(my_s + col / 2, wt);
       }
-      float la, lb;
-      unpack2(sum2, la, lb);
-      l_run += la + lb;
       tc::wait_st();
       tc::fence_before();
+      if (r == kRows - 32 && !operands_ready<KS>(p, sh, tile, w.dual ? 2 : 1, tiles0 + tiles)) return false;
       mbar_arrive(&sh.p_ready[q]);
     }
     if (steps > 0) {
@@ -951,8 +1010,11 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
       return false;
     }
 
+    float l_run, l_half;
+    unpack2(sum2, l_run, l_half);
+    l_run += l_half;
     // the row's result, or its partial when the job is cut; two streams of the same rows are joined first
-    const bool whole = w.t_begin == 0 && w.t_end == w.x.tiles;
+    const bool whole = w.t_begin == 0 && w.t_end == w.job_tiles_;
     const bool join = w.dual && tiles > 1;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (w.t_begin == 0 ? 1 : 0);
     float* xo = reinterpret_cast<float*>(exchange);  // [64 columns][128 rows]
@@ -1003,7 +1065,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         uint32_t fixed[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) fixed[k] = o[k];
-        patch_values(bad, p.v_new + (w.x.unit * p.n + w.x.tok0) * kD, min(job_row >> p.log2hg, w.x.tokens - 1), y, fixed);
+        patch_values(bad, p.v_new + (w.x.unit * p.n + w.tok0) * kD, min(job_row >> p.log2hg, w.tokens - 1), y, fixed);
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = fixed[k];
       }
@@ -1011,7 +1073,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         // column 8c + (e << 2 | i) holds channel 8c + 2i + e
         if (whole) {
           const float inv = l_run > 0.0f ? 1.0f / l_run : l_run == 0.0f ? 0.0f : l_run;
-          const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + w.x.tok0 + (job_row >> p.log2hg);
+          const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + w.tok0 + (job_row >> p.log2hg);
           uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD) + 4 * y;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1036,6 +1098,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     }
     if (join && q == 0) mbar_arrive(&sh.x_read);
     tc::fence_before();  // O is read before the next piece's first product, which waits for its queries
+    tiles0 += tiles;
     g += tiles;
   }
   return true;
@@ -1049,8 +1112,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   uint8_t* const base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sq = smem_u32(base), sk = sq + 2 * tc::kTileBytes;
   const uint32_t sv = sk + kKeyStages<ROPE> * kKeyBytes<ROPE>;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   constexpr int kIssuer = 8 + 2 * kProducers;
+  const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
+  const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -1073,6 +1139,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     sh.k_lev[tid] = p.k_lev[tid];
     sh.v_lev[tid] = p.v_lev[tid];
   }
+  if (tid == 32) {
+    sh.first = find_piece(p, g_begin);
+    reinterpret_cast<Piece*>(p.part_first)[blockIdx.x] = sh.first;
+  }
   if (warp == kIssuer) tc::alloc(&sh.tmem, kTmemColumns);
   tc::fence_before();
   __syncthreads();
@@ -1080,16 +1150,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const uint32_t tmem = sh.tmem;
   pdl_allow_next();
 
-  const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
-  const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
   bool ok = true;
   if (warp < 8) {
-    ok = softmax_role<BK != 0>(p, sh, sq, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
-  } else if (warp < 8 + kProducers) {
-    ok = key_role<BK, ROPE>(p, sh, sk, g_begin, g_end, warp - 8, lane);
+    ok = softmax_role<BK != 0, kKeyStages<ROPE>>(p, sh, sq, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
   } else if (warp < kIssuer) {
-    ok = value_role<BV>(p, sh, sv, g_begin, g_end, warp - 8 - kProducers, lane);
-  } else if (lane == 0) {
+    // keys on warp schedulers 0 and 1, values on 2 and 3: fewer different loops per instruction cache
+    const int block = ((warp - 8) >> 2) * 2 + (warp & 1);
+    if (warp & 2) ok = value_role<BV>(p, sh, sv, g_begin, g_end, block, lane);
+    else ok = key_role<BK, ROPE>(p, sh, sk, g_begin, g_end, block, lane);
+  } else {
     ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, g_begin, g_end);
   }
   if (!ok) report_error(p.err, kDevWaitTimeout);
@@ -1106,11 +1175,12 @@ constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid_constant__ ChunkParams p) {
   pdl_wait();
   const int64_t cut = ((int64_t)blockIdx.x + 1) * p.per_cta;
-  const Piece x = find_piece(p, cut);
+  const Piece x = reinterpret_cast<const Piece*>(p.part_first)[blockIdx.x + 1];
   if (x.job_start >= cut) return;              // the cut falls between two jobs
   if (cut - p.per_cta > x.job_start) return;   // an earlier cut divides the same job
-  const int64_t c0 = blockIdx.x, c1 = (x.job_start + x.tiles - 1) / p.per_cta;
-  const int hg = 1 << p.log2hg, rows = x.tokens << p.log2hg;
+  const int64_t c0 = blockIdx.x, c1 = (x.job_start + job_tiles(p, x) - 1) / p.per_cta;
+  const int64_t tok0 = job_tok0(p, x);
+  const int hg = 1 << p.log2hg, rows = job_tokens(p, x) << p.log2hg;
   const int lane = threadIdx.x & 31;
   const int64_t b = x.unit / p.Hkv, kvh = x.unit - b * p.Hkv;
   for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kMergeThreads / 32)) {
@@ -1131,12 +1201,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid
       M = m;
     }
     const float inv = L > 0.0f ? 1.0f / L : L == 0.0f ? 0.0f : L;
-    const int64_t row = (b * p.Hq + kvh * hg + (r & (hg - 1))) * p.n + x.tok0 + (r >> p.log2hg);
+    const int64_t row = (b * p.Hq + kvh * hg + (r & (hg - 1))) * p.n + tok0 + (r >> p.log2hg);
     const __half2 lo = __floats2half2_rn(a.x * inv, a.y * inv), hi = __floats2half2_rn(a.z * inv, a.w * inv);
     *reinterpret_cast<uint2*>(p.out + row * kD + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
 }
+
+constexpr int64_t kFirstBytes = 32;
+static_assert(sizeof(Piece) <= kFirstBytes, "a CTA's place in the work list");
 
 // Rows of a partial slot: a job's.
 int64_t slot_rows(int64_t n, int hg) { return n >= 2 * kRows / hg ? 2 * kRows : n * hg; }
@@ -1168,9 +1241,10 @@ cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStre
 
 }  // namespace
 
-// Two partial slots per CTA, each with the rows a job can have, of D + 2 floats a row.
+// Every CTA's place in the work list, then two partial slots per CTA, each with the rows a job can have,
+// of D + 2 floats a row.
 int64_t chunk_workspace_bytes(int64_t n, int hg, int sm_count) {
-  return 2 * (int64_t)sm_count * slot_rows(n, hg) * (kD + 2) * (int64_t)sizeof(float);
+  return (int64_t)sm_count * (kFirstBytes + 2 * slot_rows(n, hg) * (kD + 2) * (int64_t)sizeof(float));
 }
 
 cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace, int* launches, cudaStream_t s) {
@@ -1187,7 +1261,8 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   p.per_cta = (p.total_tiles + grid - 1) / grid;
   grid = (p.total_tiles + p.per_cta - 1) / p.per_cta;
   p.rows_max = (int32_t)slot_rows(p.n, hg);
-  p.part_acc = static_cast<float*>(workspace);
+  p.part_first = workspace;
+  p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + sm_count * kFirstBytes);
   p.part_ml = p.part_acc + 2 * (int64_t)sm_count * p.rows_max * kD;
   if (p.lay.frag) {
     if (p.bk == 2 && p.bv == 2) return launch_t<2, 2, false>(p, grid, launches, s);

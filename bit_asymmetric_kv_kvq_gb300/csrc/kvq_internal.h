@@ -197,6 +197,7 @@ struct ChunkParams {
   int64_t jobs_per_unit, tiles_per_unit, total_tiles, per_cta;
   int32_t log2_job_tokens;  // tokens of a job
   int32_t rows_max;         // rows a partial slot holds
+  void* part_first;         // [grid] where every CTA's part of the list begins
   float* part_acc;          // [2 * grid][rows_max][D] partial sums of jobs that CTAs share
   float* part_ml;           // [2 * grid][rows_max][2]
 };
