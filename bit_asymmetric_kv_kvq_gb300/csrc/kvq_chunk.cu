@@ -43,8 +43,11 @@ namespace {
 constexpr int kD = kHeadDim;
 constexpr int kRows = 128;   // query rows of a stream
 constexpr int kTile = 128;   // keys of a tile
-constexpr int kProducers = 4;  // warps that make key tiles, and as many that make value tiles
-constexpr int kThreads = (8 + 2 * kProducers + 1) * 32;
+constexpr int kProducers = 4;  // warps that make a key tile, and as many that make a value tile: a 32-token block each
+template <bool ROPE>
+constexpr int kKeySets = ROPE ? 2 : 1;  // sets of key producers, taking turns at the tiles
+template <bool ROPE>
+constexpr int kThreads = (8 + (kKeySets<ROPE> + 1) * kProducers + 1) * 32;
 constexpr float kLazy = 8.0f;      // log2 units the running maximum may lag behind
 constexpr float kWeightExp = 7.0f; // weights are at most 2^(8 + 7): below fp16's 65504
 constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O at 256 and 384
@@ -64,7 +67,9 @@ struct __align__(16) Shared {
   uint32_t tmem;
   uint32_t bad[kBadSlots][8];  // tokens of the job with a non-finite value that some of its rows must not see
   __half2 mu[kD / 2];          // per channel pair
-  alignas(16) uint32_t k_meta[2][kProducers][128], v_meta[2][kProducers][128];  // zero points and steps of two tiles' blocks
+  alignas(16) uint32_t k_meta[2][2][kProducers][128], v_meta[2][kProducers][128];  // zero points and steps of two tiles' blocks
+  alignas(8) uint8_t lo_slot[2][kProducers][64];  // rotated keys: a pair's place in the low tile, or 255
+  alignas(16) unsigned long long turns[kD / 2];  // rotated keys: the turn per token of every pair
   float k_lev[16], v_lev[16];
   float xm[kRows], xl[kRows];  // the second stream's m and l
 };
@@ -262,25 +267,83 @@ __device__ __forceinline__ void store_frag_row(uint32_t tile, int row, int q, co
     sts16(tile + tc::chunk_offset(q / 2, row, 2 * t + (q & 1)), x[t], x[4 + t], x[8 + t], x[12 + t]);
 }
 
-__device__ __forceinline__ float2 key_turn(const ChunkParams& p, int64_t pos, int i) {
-  const unsigned long long t = (unsigned long long)pos * p.rope_turns[i];
-  float s, c;
-  sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s, &c);
-  return make_float2(c, s);
+// Cosine and sine of frequency i at a position: the turn's fraction in 0.32 fixed point (position times the 0.64
+// fraction of a turn per token, whole turns dropped), then the approximations, which are off by 2^-20.5 at most.
+__device__ __forceinline__ float2 key_turn(uint32_t pos, uint2 t) {
+  const float a = (float)(int32_t)(pos * t.y + __umulhi(pos, t.x)) * (6.28318530718f / 4294967296.0f);
+  return make_float2(__cosf(a), __sinf(a));
+}
+
+// Rotated keys: the eight pairs whose channels are largest in a sample of the unit's keys -- one page's ranges, or
+// the first fp16 rows when there is no page -- have their fp16 rounding made up for by a second, 16-channel tile
+// that holds what it left over.  Every lane returns pairs 2 lane, 2 lane + 1's places in it (255: none).
+__device__ __forceinline__ uint2 low_places(const ChunkParams& p, const uint8_t* unit_pages, const uint16_t* rows,
+                                            const uint16_t* fresh, int lane) {
+  float size[2] = {0.0f, 0.0f};
+  if (p.n_pages > 0) {
+    const uint32_t* m =
+        reinterpret_cast<const uint32_t*>(unit_pages + (p.n_pages / 2) * p.lay.bytes + p.lay.off_km);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const __half2 v = h2(__ldg(m + 2 * lane + (c & 1) + 64 * (c >> 1)));
+      const float z = __low2float(v), top = z + __high2float(v) * (float)((1 << p.bk) - 1);
+      size[c & 1] = fmaxf(size[c & 1], fmaxf(fabsf(z), fabsf(top)));
+    }
+    // sparse entries are outside those ranges: those of 32 tokens
+    const uint8_t* pg = unit_pages + (p.n_pages / 2) * p.lay.bytes;
+#pragma unroll 1
+    for (int e = 0; e < p.nsp; ++e) {
+      const uint32_t mine = ((uint32_t)(pg[p.lay.off_si + lane * p.nsp + e] & 63) << 16) |
+                            (reinterpret_cast<const uint16_t*>(pg + p.lay.off_sv)[lane * p.nsp + e] & 0x7FFFu);
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t x = __shfl_sync(0xffffffffu, mine, i);
+        const float v = __half2float(__ushort_as_half((uint16_t)x));
+        if ((int)(x >> 17) == lane) {
+          if ((x >> 16) & 1u) size[1] = fmaxf(size[1], v);
+          else size[0] = fmaxf(size[0], v);
+        }
+      }
+    }
+  } else {
+    const int64_t total = p.n_w + p.n;
+    for (int64_t j = 0; j < 16 && j < total; ++j) {
+      const uint32_t* r = reinterpret_cast<const uint32_t*>(j < p.n_w ? rows + j * kD : fresh + (j - p.n_w) * kD);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float2 v = __half22float2(h2(__ldg(r + lane + 32 * c)));
+        size[0] = fmaxf(size[0], fabsf(v.x));
+        size[1] = fmaxf(size[1], fabsf(v.y));
+      }
+    }
+  }
+  uint2 place = make_uint2(255, 255);
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    // the largest left over; sizes are >= 0, so their bits order them, and the low bits break ties
+    const uint32_t a = place.x == 255 ? (__float_as_uint(size[0]) & ~127u) | (127 - 2 * lane) : 0;
+    const uint32_t b = place.y == 255 ? (__float_as_uint(size[1]) & ~127u) | (126 - 2 * lane) : 0;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(a, b));
+    if (a == top) place.x = k;
+    else if (b == top) place.y = k;
+  }
+  return place;
 }
 
 // Eight channels 8q + k and their rotation partners 64 + 8q + k of a key row, fp32, into the key tile
-// (channel order as it is): rotated and split into hi + lo, or shifted by mu.
+// (channel order as it is): rotated, with what fp16 leaves over of eight chosen pairs in the low tile, or shifted
+// by mu.
 template <bool ROPE>
 __device__ __forceinline__ void store_key_octets(const ChunkParams& p, const Shared& sh, uint32_t tile, int row, int q,
-                                                 int64_t pos, float (&x)[8], float (&y)[8]) {
-  uint32_t hx[4], hy[4], lx[4], ly[4];
+                                                 uint32_t pos, const uint8_t* lo_slot, float (&x)[8], float (&y)[8]) {
+  uint32_t hx[4], hy[4];
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     if constexpr (ROPE) {
+      const uint4 tt = reinterpret_cast<const uint4*>(sh.turns)[4 * q + k / 2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float2 cs = key_turn(p, pos, 8 * q + k + e);
+        const float2 cs = key_turn(pos, e ? make_uint2(tt.z, tt.w) : make_uint2(tt.x, tt.y));
         const float a = x[k + e] * cs.x - y[k + e] * cs.y, b = x[k + e] * cs.y + y[k + e] * cs.x;
         x[k + e] = a;
         y[k + e] = b;
@@ -295,17 +358,92 @@ __device__ __forceinline__ void store_key_octets(const ChunkParams& p, const Sha
     const __half2 a = __floats2half2_rn(x[k], x[k + 1]), b = __floats2half2_rn(y[k], y[k + 1]);
     hx[k / 2] = u32(a);
     hy[k / 2] = u32(b);
-    if constexpr (ROPE) {
-      const float2 fa = __half22float2(a), fb = __half22float2(b);
-      lx[k / 2] = u32(__floats2half2_rn(x[k] - fa.x, x[k + 1] - fa.y));
-      ly[k / 2] = u32(__floats2half2_rn(y[k] - fb.x, y[k + 1] - fb.y));
-    }
   }
   sts16(tile + tc::chunk_offset(0, row, q), hx[0], hx[1], hx[2], hx[3]);
   sts16(tile + tc::chunk_offset(1, row, q), hy[0], hy[1], hy[2], hy[3]);
   if constexpr (ROPE) {
-    sts16(tile + tc::kTileBytes + tc::chunk_offset(0, row, q), lx[0], lx[1], lx[2], lx[3]);
-    sts16(tile + tc::kTileBytes + tc::chunk_offset(1, row, q), ly[0], ly[1], ly[2], ly[3]);
+    const uint2 slots = *reinterpret_cast<const uint2*>(lo_slot + 8 * q);
+    if ((slots.x & slots.y) != 0xFFFFFFFFu) {  // the octet holds one of the eight pairs
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t j = ((k < 4 ? slots.x : slots.y) >> (8 * (k & 3))) & 255u;
+        if (j != 255u) {
+          const float2 fa = __half22float2(h2(hx[k / 2])), fb = __half22float2(h2(hy[k / 2]));
+          const uint32_t lo = tile + tc::kTileBytes;
+          sts2(lo + tc::offset16(row, j), __half_as_ushort(__float2half_rn(x[k] - (k & 1 ? fa.y : fa.x))));
+          sts2(lo + tc::offset16(row, 8 + j), __half_as_ushort(__float2half_rn(y[k] - (k & 1 ? fb.y : fb.x))));
+        }
+      }
+    }
+  }
+}
+
+// A code as a float: its bits in the mantissa of 2^23, less 2^23.
+__device__ __forceinline__ float code_float(uint32_t codes, int shift, uint32_t mask) {
+  return __uint_as_float(((codes >> shift) & mask) | 0x4B000000u) - 8388608.0f;
+}
+
+// Keys of a 32-token block of a bitstream page, for one warp: lane = token, its row of codes in registers, an
+// octet of channels and their rotation partners at a time.  meta: the group's 128 zero point / step words in
+// shared memory.
+template <bool ROPE, bool LUT>
+__device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
+                                               int slot, const uint4* meta, uint32_t pos, const uint8_t* lo_slot,
+                                               uint32_t tile, int lane) {
+  const int bits = p.bk, tk = 32 * block + lane, row = 32 * slot + lane;
+  const uint32_t mask = (1u << bits) - 1u;
+  uint32_t w[2][8] = {};  // codes of channels 0..63 and 64..127: 2 * bits words each
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < bits) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(page + p.lay.off_kc) + (tk * 2 + h) * bits + i);
+        w[h][2 * i] = v.x;
+        w[h][2 * i + 1] = v.y;
+      }
+  uint32_t sp[4];  // sparse entries: channel << 16 | fp16 bits
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    sp[e] = 0xFFFFFFFFu;
+    if (e < p.nsp)
+      sp[e] = (uint32_t)page[p.lay.off_si + tk * p.nsp + e] << 16 |
+              reinterpret_cast<const uint16_t*>(page + p.lay.off_sv)[tk * p.nsp + e];
+  }
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    float x[8], y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float(&o)[8] = h ? y : x;
+      const uint4 ma = meta[16 * h + 2 * q], mb = meta[16 * h + 2 * q + 1];
+      const uint32_t m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 zs = __half22float2(h2(m[k]));
+        const float c = LUT ? sh.k_lev[(w[h][0] >> (bits * k)) & mask] : code_float(w[h][0], bits * k, mask);
+        o[k] = fmaf(zs.y, c, zs.x);
+      }
+      // the next octet's codes to the front
+#pragma unroll
+      for (int i = 0; i < 7; ++i) w[h][i] = __funnelshift_rc(w[h][i], w[h][i + 1], 8 * bits);
+      w[h][7] = __funnelshift_rc(w[h][7], 0u, 8 * bits);
+    }
+#pragma unroll 1
+    for (int e = 0; e < p.nsp; ++e) {
+      const uint32_t s = e == 0 ? sp[0] : e == 1 ? sp[1] : e == 2 ? sp[2] : sp[3];
+      if (((s >> 19) & 7u) != (uint32_t)q) continue;  // of this octet or its partner
+      const float v = __half2float(__ushort_as_half((uint16_t)s));
+      const int k0 = (s >> 16) & 7;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k == k0) {
+          if (s >> 22) y[k] = v;
+          else x[k] = v;
+        }
+      }
+    }
+    store_key_octets<ROPE>(p, sh, tile, row, q, pos, lo_slot, x, y);
   }
 }
 
@@ -316,95 +454,45 @@ __device__ __forceinline__ uint32_t octet(const uint32_t* row, int bits, int oct
   return __funnelshift_r(lo, hi, off & 31);
 }
 
-// Key tile of bitstream pages: lane = token, one octet pair of channels at a time.
-template <bool ROPE>
-__device__ __forceinline__ void key_tile_bits(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
-                                              int64_t page0, uint32_t tile, int warp, int lane) {
-  const int bits = p.bk, mask = (1 << bits) - 1;
-  for (int task = warp; task < 32; task += kProducers) {
-    const int q = task >> 2, tok = 32 * (task & 3) + lane;
-    const int in_tile = tok / p.R;
-    const int64_t page = page0 + in_tile;
-    float x[8], y[8];
-    int64_t pos = 0;
-    if (in_tile < p.pages_per_tile && page < p.n_pages) {
-      const int tk = tok - in_tile * p.R;
-      const uint8_t* pg = unit_pages + page * p.lay.bytes;
-      pos = p.n_s + page * p.R + tk;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(pg + p.lay.off_kc) + tk * 4 * bits;
-      const uint32_t cx = octet(row, bits, q), cy = octet(row, bits, q + 8);
-      const uint4* mp = reinterpret_cast<const uint4*>(pg + p.lay.off_km) + (tk / p.G) * (kD / 4);
-      uint4 mv[4] = {__ldg(mp + 2 * q), __ldg(mp + 2 * q + 1), __ldg(mp + 16 + 2 * q), __ldg(mp + 17 + 2 * q)};
-      const uint32_t* m = reinterpret_cast<const uint32_t*>(mv);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const __half2 a = h2(m[k]), b = h2(m[8 + k]);
-        const int ca = (cx >> (bits * k)) & mask, cb = (cy >> (bits * k)) & mask;
-        const float fa = p.lut ? sh.k_lev[ca] : (float)ca, fb = p.lut ? sh.k_lev[cb] : (float)cb;
-        x[k] = fmaf(__high2float(a), fa, __low2float(a));
-        y[k] = fmaf(__high2float(b), fb, __low2float(b));
-      }
-      for (int e = 0; e < p.nsp; ++e) {
-        const int c = pg[p.lay.off_si + tk * p.nsp + e];
-        const float v = __half2float(__ushort_as_half(reinterpret_cast<const uint16_t*>(pg + p.lay.off_sv)[tk * p.nsp + e]));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (c == 8 * q + k) x[k] = v;
-          if (c == 64 + 8 * q + k) y[k] = v;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = y[k] = 0.0f;
-    }
-    store_key_octets<ROPE>(p, sh, tile, tok, q, pos, x, y);
-  }
-}
-
-// Value tile of bitstream pages: lane = two neighbouring tokens, one octet of channels at a time.
-__device__ __forceinline__ void value_tile_bits(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
-                                                int64_t page0, uint32_t tile, int warp, int lane) {
-  const int bits = p.bv, mask = (1 << bits) - 1;
-  for (int task = warp; task < 32; task += kProducers) {
-    const int q = task >> 1, tp = 32 * (task & 1) + lane, tok = 2 * tp;
-    const int in_tile = tok / p.R;
-    const int64_t page = page0 + in_tile;
+// Values of a 32-token block of a bitstream page, for one warp: lane = two neighbouring tokens of every second octet
+// of channels.  meta: the block's [32 tokens][D/G] zero point / step words in shared memory; page null: zeros.
+template <bool LUT>
+__device__ __forceinline__ void value_block_bits(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
+                                                 int slot, const uint32_t* meta, uint32_t tile, int lane) {
+  const int bits = p.bv, tp = lane & 15, per_token = kD / p.G;
+  const uint32_t mask = (1u << bits) - 1u;
+  const uint32_t* row =
+      page ? reinterpret_cast<const uint32_t*>(page + p.lay.off_vc) + (32 * block + 2 * tp) * 4 * bits : nullptr;
+#pragma unroll 1
+  for (int it = 0; it < 8; ++it) {
+    const int q = 2 * it + (lane >> 4);
     uint32_t o[8] = {};
-    if (in_tile < p.pages_per_tile && page < p.n_pages) {
-      const int tk = tok - in_tile * p.R;
-      const uint8_t* pg = unit_pages + page * p.lay.bytes;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(pg + p.lay.off_vc) + tk * 4 * bits;
+    if (page) {
       const uint32_t c0 = octet(row, bits, q), c1 = octet(row + 4 * bits, bits, q);
-      const uint32_t* m = reinterpret_cast<const uint32_t*>(pg + p.lay.off_vm) + tk * (kD / p.G) + 8 * q / p.G;
-      const __half2 a = h2(__ldg(m)), b = h2(__ldg(m + kD / p.G));
+      const uint32_t* m = meta + 2 * tp * per_token + 8 * q / p.G;
+      const float2 a = __half22float2(h2(m[0])), b = __half22float2(h2(m[per_token]));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i0 = (c0 >> (bits * k)) & mask, i1 = (c1 >> (bits * k)) & mask;
-        const float f0 = p.lut ? sh.v_lev[i0] : (float)i0, f1 = p.lut ? sh.v_lev[i1] : (float)i1;
-        o[k] = u32(__floats2half2_rn(fmaf(__high2float(a), f0, __low2float(a)), fmaf(__high2float(b), f1, __low2float(b))));
+        const float f0 = LUT ? sh.v_lev[(c0 >> (bits * k)) & mask] : code_float(c0, bits * k, mask);
+        const float f1 = LUT ? sh.v_lev[(c1 >> (bits * k)) & mask] : code_float(c1, bits * k, mask);
+        o[k] = u32(__floats2half2_rn(fmaf(a.y, f0, a.x), fmaf(b.y, f1, b.x)));
       }
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      sts4(tile + tc::chunk_offset(tp >> 5, value_row(8 * q + k), (tp & 31) >> 2) + 4 * (tp & 3), o[k]);
+      sts4(tile + tc::chunk_offset(slot >> 1, value_row(8 * q + k), 4 * (slot & 1) + (tp >> 2)) + 4 * (tp & 3), o[k]);
   }
 }
 
-// Sparse entries of fragment-order pages, over the dense keys already in the tile.
-__device__ __forceinline__ void sparse_keys(const ChunkParams& p, const Shared& sh, const uint8_t* unit_pages,
-                                            int64_t page0, uint32_t tile, int tid) {
-  for (int i = tid; i < kTile * p.nsp; i += kProducers * 32) {
-    const int tok = i / p.nsp, e = i - tok * p.nsp;
-    const int in_tile = tok / p.R;
-    const int64_t page = page0 + in_tile;
-    if (in_tile >= p.pages_per_tile || page >= p.n_pages) continue;
-    const int tk = tok - in_tile * p.R;
-    const uint8_t* pg = unit_pages + page * p.lay.bytes;
+// Sparse entries of a 32-token block of a fragment-order page, over the dense keys the warp has written.
+__device__ __forceinline__ void sparse_block(const ChunkParams& p, const Shared& sh, const uint8_t* pg, int block,
+                                             int slot, uint32_t tile, int lane) {
+  const int tk = 32 * block + lane;
+  const int row = 32 * slot + 8 * ((lane & 7) >> 1) + 4 * (lane >> 4) + 2 * ((lane >> 3) & 1) + (lane & 1);
+  for (int e = 0; e < p.nsp; ++e) {
     const int c = pg[p.lay.off_si + tk * p.nsp + e];
     const float v = __half2float(__ushort_as_half(reinterpret_cast<const uint16_t*>(pg + p.lay.off_sv)[tk * p.nsp + e]));
     const float m = __half2float(reinterpret_cast<const __half*>(sh.mu)[c]);
-    const int x = tok & 31;  // 16a + 8b + 2t' + e'
-    const int row = (tok & ~31) + 8 * ((x & 7) >> 1) + 4 * (x >> 4) + 2 * ((x >> 3) & 1) + (x & 1);
     sts2(tile + frag_column(row, c), __half_as_ushort(__float2half_rn(v - m)));
   }
 }
@@ -417,24 +505,24 @@ __device__ __forceinline__ const uint16_t* f16_row(const uint16_t* rows, const u
 // Keys of an fp16 tile: rows j0 .. j0 + 127 of the list, zeros from `end` on.
 template <bool FRAG, bool ROPE>
 __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared& sh, const uint16_t* rows,
-                                             const uint16_t* fresh, int64_t j0, int64_t end, uint32_t tile, int warp,
-                                             int lane) {
+                                             const uint16_t* fresh, int64_t j0, int64_t end, const uint8_t* lo_slot,
+                                             uint32_t tile, int warp, int lane) {
   if constexpr (FRAG) {
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {  // two rows' loads in flight per lane
       uint4 v[2][4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane >> 2);
+        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane & 7);  // eight rows: all banks of a store
         if (j0 + row < end) {
-          const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j0 + row)) + 4 * (lane & 3);
+          const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j0 + row)) + 4 * (lane >> 3);
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[h][i] = __ldg(src + i);
         }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane >> 2), q = lane & 3;
+        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane & 7), q = lane >> 3;
         uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
         if (j0 + row < end) {
 #pragma unroll
@@ -444,12 +532,15 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
       }
     }
   } else {
-    for (int task = warp; task < 32; task += kProducers) {
-      const int q = task >> 2, row = 32 * (task & 3) + lane;
-      const int64_t j = j0 + row;
+    const int row = 32 * warp + lane;
+    const int64_t j = j0 + row;
+    // positions: the sink's rows first, the window behind the quantized tokens, then the new tokens
+    const uint32_t pos = (uint32_t)(j < p.n_s ? j : j + p.Tq);
+    const uint4* src = j < end ? reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j)) : nullptr;
+#pragma unroll 2
+    for (int q = 0; q < 8; ++q) {
       float x[8] = {}, y[8] = {};
-      if (j < end) {
-        const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j));
+      if (src) {
         const uint4 vx = __ldg(src + q), vy = __ldg(src + 8 + q);
         const __half2 *hx = reinterpret_cast<const __half2*>(&vx), *hy = reinterpret_cast<const __half2*>(&vy);
 #pragma unroll
@@ -461,8 +552,7 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
           y[2 * k + 1] = b.y;
         }
       }
-      // positions: the sink's rows first, the window behind the quantized tokens, then the new tokens
-      store_key_octets<ROPE>(p, sh, tile, row, q, j < p.n_s ? j : j + p.Tq, x, y);
+      store_key_octets<ROPE>(p, sh, tile, row, q, pos, lo_slot, x, y);
     }
   }
 }
@@ -509,8 +599,10 @@ __device__ __forceinline__ void value_tile_f16(const ChunkParams& p, uint32_t* b
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t sel = e ? 0x7632 : 0x5410;
-        sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + e), oct & 7), __byte_perm(x[h][0], x[h][1], sel),
+        // lanes 4..7 of every eight begin with their odd channel, so the eight rows are on different banks
+        const int odd = e ^ ((lane >> 2) & 1);
+        const uint32_t sel = odd ? 0x7632 : 0x5410;
+        sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + odd), oct & 7), __byte_perm(x[h][0], x[h][1], sel),
               __byte_perm(x[h][2], x[h][3], sel), __byte_perm(x[h][4], x[h][5], sel), __byte_perm(x[h][6], x[h][7], sel));
       }
     }
@@ -565,12 +657,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ------------------------------------------------------------ the kernel
 
+constexpr int kKeyStages = 2;
+template <bool ROPE>  // a rotated key tile has a low tile behind it, and so have the queries' tiles, behind all others
+constexpr int kKeyBytes = tc::kTileBytes + (ROPE ? tc::kTile16Bytes : 0);
 template <bool ROPE>
-constexpr int kKeyStages = ROPE ? 1 : 2;  // a rotated key tile is two tiles, hi and lo
-template <bool ROPE>
-constexpr int kKeyBytes = (ROPE ? 2 : 1) * tc::kTileBytes;
-template <bool ROPE>
-constexpr int kSmemBytes = 2 * tc::kTileBytes + kKeyStages<ROPE> * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
+constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
+static_assert(kKeyBytes<true> % 1024 == 0 && kKeySets<true> == kKeyStages, "a set of key producers per stage");
 
 // A CTA's walk over its pieces of the work list: what every role needs to know of one.
 struct Walk {
@@ -614,8 +706,8 @@ __device__ __forceinline__ bool wait(const ChunkParams& p, uint64_t* bar, uint32
   return true;
 }
 
-// Barrier among the warps of one role, with the time limit of every wait (a hardware barrier has none).
-__device__ __forceinline__ bool sync_role(const ChunkParams& p, uint64_t* bar, uint32_t* count) {
+// Barrier among warps of one role, with the time limit of every wait (a hardware barrier has none).
+__device__ __forceinline__ bool meet(const ChunkParams& p, uint64_t* bar, uint32_t* count) {
   mbar_arrive(bar);
   return wait(p, bar, (*count)++ & 1);
 }
@@ -623,18 +715,17 @@ __device__ __forceinline__ bool sync_role(const ChunkParams& p, uint64_t* bar, u
 // The value of lane 0, known to be the same in every lane.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// One product of a stream with a tile: S = Q K^T (hi and lo halves of rotated keys), or O (+)= P V.  A
+// One product of a stream with a tile: S = Q K^T (rotated keys with their low tile), or O (+)= P V.  A
 // descriptor's high word is the same for every tile; the low word moves by 2 (32 bytes) with every 16
 // columns and by a block's size after 64.
 template <bool ROPE>
-__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k) {
+__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint64_t q_lo, uint64_t k_lo) {
 #pragma unroll
-  for (int h = 0; h < (ROPE ? 2 : 1); ++h)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t off = ((i >> 2) * tc::kBlockBytes + (i & 3) * 32) >> 4;
-      tc::mma_ss(d, q + off, k + (h * (tc::kTileBytes >> 4) + off), tc::instruction(kTile), h > 0 || i > 0);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t off = ((i >> 2) * tc::kBlockBytes + (i & 3) * 32) >> 4;
+    tc::mma_ss(d, q + off, k + off, tc::instruction(kTile), i > 0);
+  }
+  if constexpr (ROPE) tc::mma_ss(d, q_lo, k_lo, tc::instruction(kTile), true);
 }
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint64_t v, bool accumulate) {
 #pragma unroll
@@ -653,10 +744,11 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint64_t v, 
 template <bool ROPE>
 __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sk, uint32_t sv,
                                            uint32_t tmem_, int64_t g_begin, int64_t g_end) {
-  constexpr int KS = kKeyStages<ROPE>;
+  constexpr int KS = kKeyStages;
   const bool leader = tc::elect();
   const uint32_t tmem = uniform(tmem_);
   const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv);
+  const uint64_t dq_lo = tc::descriptor16(sv + kValueStages * tc::kTileBytes), dk_lo = tc::descriptor16(sk + tc::kTileBytes);
   uint32_t kt = 0, vt = 0, jobs = 0, used0 = 0, used1 = 0;  // key and value tiles, pieces, steps of the streams so far
   Walk w(sh.first);
   bool more = g_begin < g_end;
@@ -685,7 +777,8 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
           if (last) tc::commit(&sh.v_empty[vs]);
         }
         if (s + 2 < steps) {
-          issue_qk<ROPE>(tmem + at, dq + (dual ? 0 : q * (tc::kTileBytes >> 4)), dk + ks * (kKeyBytes<ROPE> >> 4));
+          issue_qk<ROPE>(tmem + at, dq + (dual ? 0 : q * (tc::kTileBytes >> 4)), dk + ks * (kKeyBytes<ROPE> >> 4),
+                         dq_lo + (dual ? 0 : q * (tc::kTile16Bytes >> 4)), dk_lo + ks * (kKeyBytes<ROPE> >> 4));
           tc::commit(&sh.s_full[q]);
         } else if (s >= 0) {
           tc::commit(&sh.o_done[q]);
@@ -703,22 +796,31 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
   return true;
 }
 
-// Key producers: warp 0..3.
-template <int BK, bool ROPE>
+// Key producers: warp 0..3 of a set.
+template <int BK, bool ROPE, bool LUT>
 __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int64_t g_begin, int64_t g_end,
-                                         int warp, int lane) {
+                                         int set, int warp, int lane) {
   constexpr bool FRAG = BK != 0;
-  constexpr int KS = kKeyStages<ROPE>;
+  constexpr int KS = kKeyStages, SETS = kKeySets<ROPE>;
   const int tid = 32 * warp + lane;
-  uint32_t kt = 0, syncs = 0;
+  uint32_t kt0 = 0, syncs = 0;
+  // the warp's 32-token block: its page of a tile and its place in the page
+  const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32;
   Walk w(sh.first);
   for (int64_t g = g_begin; g < g_end; w.next(p)) {
     w.at(p, g, g_end);
     const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
     const uint16_t* rows = p.wk + w.x.unit * p.win_unit_stride;
     const uint16_t* fresh = p.k_new + w.x.unit * p.n * kD;
-    if constexpr (!ROPE) {  // mu: the centre of each channel's range in one page of the unit
-      if (!sync_role(p, &sh.k_sync, &syncs)) return false;  // the last piece's tiles no longer need the old one
+    uint8_t* lo_slot = sh.lo_slot[set][warp];
+    if constexpr (ROPE) {
+      const uint2 place = low_places(p, unit_pages, rows, fresh, lane);
+      __syncwarp();
+      lo_slot[2 * lane] = (uint8_t)place.x;
+      lo_slot[2 * lane + 1] = (uint8_t)place.y;
+      __syncwarp();
+    } else {  // mu: the centre of each channel's range in one page of the unit
+      if (!meet(p, &sh.k_sync, &syncs)) return false;  // the last piece's tiles no longer need the old one
       float mu = 0.0f;
       if (p.n_pages > 0) {
         const uint8_t* pg = unit_pages + (p.n_pages / 2) * p.lay.bytes;
@@ -728,72 +830,87 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
         if (fabsf(centre) > range && fabsf(centre) <= 4096.0f) mu = centre;
       }
       reinterpret_cast<__half*>(sh.mu)[tid] = __float2half_rn(mu);
-      if (!sync_role(p, &sh.k_sync, &syncs)) return false;
+      if (!meet(p, &sh.k_sync, &syncs)) return false;
     }
-    // fragment-order pages: the next tile's codes wait in registers and its meta words in shared memory
-    constexpr int NW = FRAG ? 4 * BK : 4;
+    // the next tile's meta words are on their way to shared memory, and its codes to registers (fragment order) or L2
+    constexpr int NW = FRAG ? 4 * BK : 1;
     uint32_t next[NW];
-    int in_tile = 0, block = 0;  // page of the tile and 32-token block of the page that this warp expands
-    auto fetch = [&](int64_t t) {
-      if constexpr (FRAG) {
-        const int64_t page = t * p.pages_per_tile + in_tile;
-        if (in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages) {
-          const uint8_t* pg = unit_pages + page * p.lay.bytes;
-          load_codes<BK>(pg + p.lay.off_kc, block, lane, next);
-          cp_async16(&sh.k_meta[t & 1][warp][4 * lane], pg + p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane);
-        }
-        cp_async_commit();
-      }
+    auto page_of = [&](int64_t t) -> const uint8_t* {
+      const int64_t page = t * p.pages_per_tile + in_tile;
+      return in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages ? unit_pages + page * p.lay.bytes : nullptr;
     };
-    if constexpr (FRAG) {
-      in_tile = 32 * warp / p.R;
-      block = (32 * warp - in_tile * p.R) / 32;
-      fetch(w.t_begin);
-    }
-    for (int64_t t = w.t_begin; t < w.t_end; ++t, ++kt) {
-      const uint32_t st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
+    auto fetch = [&](int64_t t) {
+      if (const uint8_t* pg = page_of(t)) {
+        if constexpr (FRAG) {
+          load_codes<BK>(pg + p.lay.off_kc, block, lane, next);
+        } else if (128 * lane < 512 * p.bk) {  // the block's 512 * bits bytes
+          prefetch_l2(pg + p.lay.off_kc + block * 512 * p.bk + 128 * lane);
+        }
+        cp_async16(&sh.k_meta[set][(t / SETS) & 1][warp][4 * lane],
+                   pg + p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane);
+      }
+      cp_async_commit();
+    };
+    const int64_t first = w.t_begin + (SETS == 1 ? 0 : (kt0 ^ (uint32_t)set) & 1);  // this set's first tile
+    fetch(first);
+    for (int64_t t = first; t < w.t_end; t += SETS) {
+      const uint32_t kt = kt0 + (uint32_t)(t - w.t_begin), st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
       uint32_t codes[NW];
 #pragma unroll
       for (int i = 0; i < NW; ++i) codes[i] = next[i];
-      fetch(t + 1);
+      fetch(t + SETS);
       if (!wait(p, &sh.k_empty[st], ((kt / KS) & 1) ^ 1)) return false;
       if (t < p.page_tiles) {
-        const int64_t page0 = t * p.pages_per_tile;
+        const uint8_t* pg = page_of(t);
+        const uint32_t* meta = sh.k_meta[set][(t / SETS) & 1][warp];
+        cp_async_wait<1>();
+        __syncwarp();
         if constexpr (FRAG) {
-          if (in_tile < p.pages_per_tile && page0 + in_tile < p.n_pages) {
-            cp_async_wait<1>();
-            __syncwarp();
-            key_block<BK>(codes, reinterpret_cast<const uint2*>(sh.k_meta[t & 1][warp]), sh.mu, warp, tile, lane);
+          if (pg) {
+            key_block<BK>(codes, reinterpret_cast<const uint2*>(meta), sh.mu, warp, tile, lane);
+            if (p.nsp > 0) {
+              __syncwarp();
+              sparse_block(p, sh, pg, block, warp, tile, lane);
+            }
           } else {
             for (int i = lane; i < 32 * 16; i += 32)
               sts16(tile + tc::chunk_offset(i >> 8, 32 * warp + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
           }
-          if (p.nsp > 0) {
-            if (!sync_role(p, &sh.k_sync, &syncs)) return false;
-            sparse_keys(p, sh, unit_pages, page0, tile, tid);
-          }
         } else {
-          key_tile_bits<ROPE>(p, sh, unit_pages, page0, tile, warp, lane);
+          if (pg) {
+            const int64_t page = t * p.pages_per_tile + in_tile;
+            key_block_bits<ROPE, LUT>(p, sh, pg, block, warp, reinterpret_cast<const uint4*>(meta),
+                                      (uint32_t)(p.n_s + page * p.R + 32 * block + lane), lo_slot, tile, lane);
+          } else {
+            for (int i = lane; i < 32 * 16; i += 32)
+              sts16(tile + tc::chunk_offset(i >> 8, 32 * warp + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
+            if constexpr (ROPE) {
+              for (int i = lane; i < 32 * 2; i += 32)
+                sts16(tile + tc::kTileBytes + 32 * 32 * warp + 16 * i, 0, 0, 0, 0);
+            }
+          }
         }
       } else {
-        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, tile, warp,
-                                 lane);
+        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, lo_slot,
+                                 tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && (int64_t)kt != (int64_t)p.test_withhold - 1) mbar_arrive(&sh.k_full[st]);
     }
+    kt0 += (uint32_t)w.tiles();
     g += w.tiles();
   }
   return true;
 }
 
 // Value producers: warp 0..3.
-template <int BV>
+template <int BV, bool LUT>
 __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int64_t g_begin, int64_t g_end,
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
+  const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32, half = p.G == 64 ? 1 : 0;
   Walk w(sh.first);
   for (int64_t g = g_begin; g < g_end; ++jobs, w.next(p)) {
     w.at(p, g, g_end);
@@ -802,28 +919,26 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
     const uint16_t* fresh = p.v_new + w.x.unit * p.n * kD;
     uint32_t* bad = sh.bad[jobs % kBadSlots];
     if (warp == 0 && lane < 8) bad[lane] = 0;
-    if (!sync_role(p, &sh.v_sync, &syncs)) return false;
-    constexpr int NW = FRAG ? 4 * BV : 4;
+    if (!meet(p, &sh.v_sync, &syncs)) return false;
+    constexpr int NW = FRAG ? 4 * BV : 1;
     uint32_t next[NW];
-    int in_tile = 0, block = 0;
-    const int half = p.G == 64 ? 1 : 0;
-    auto fetch = [&](int64_t t) {
-      if constexpr (FRAG) {
-        const int64_t page = t * p.pages_per_tile + in_tile;
-        if (in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages) {
-          const uint8_t* pg = unit_pages + page * p.lay.bytes;
-          load_codes<BV>(pg + p.lay.off_vc, block, lane, next);
-          if (lane < (32 >> half))
-            cp_async16(&sh.v_meta[t & 1][warp][4 * lane], pg + p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane);
-        }
-        cp_async_commit();
-      }
+    auto page_of = [&](int64_t t) -> const uint8_t* {
+      const int64_t page = t * p.pages_per_tile + in_tile;
+      return in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages ? unit_pages + page * p.lay.bytes : nullptr;
     };
-    if constexpr (FRAG) {
-      in_tile = 32 * warp / p.R;
-      block = (32 * warp - in_tile * p.R) / 32;
-      fetch(w.t_begin);
-    }
+    auto fetch = [&](int64_t t) {
+      if (const uint8_t* pg = page_of(t)) {
+        if constexpr (FRAG) {
+          load_codes<BV>(pg + p.lay.off_vc, block, lane, next);
+        } else if (128 * lane < 512 * p.bv) {
+          prefetch_l2(pg + p.lay.off_vc + block * 512 * p.bv + 128 * lane);
+        }
+        if (lane < (32 >> half))
+          cp_async16(&sh.v_meta[t & 1][warp][4 * lane], pg + p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane);
+      }
+      cp_async_commit();
+    };
+    fetch(w.t_begin);
     for (int64_t t = w.t_begin; t < w.t_end; ++t, ++kt) {
       const uint32_t st = kt % kValueStages, tile = sv + st * tc::kTileBytes;
       uint32_t codes[NW];
@@ -832,18 +947,18 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
       fetch(t + 1);
       if (!wait(p, &sh.v_empty[st], ((kt / kValueStages) & 1) ^ 1)) return false;
       if (t < p.page_tiles) {
-        const int64_t page0 = t * p.pages_per_tile;
+        const uint8_t* pg = page_of(t);
+        cp_async_wait<1>();
+        __syncwarp();
         if constexpr (FRAG) {
-          if (in_tile < p.pages_per_tile && page0 + in_tile < p.n_pages) {
-            cp_async_wait<1>();
-            __syncwarp();
+          if (pg) {
             value_block<BV>(codes, sh.v_meta[t & 1][warp], half, warp, tile, lane);
           } else {
             for (int i = lane; i < 128 * 4; i += 32)
               sts16(tile + tc::chunk_offset(warp >> 1, i >> 2, 4 * (warp & 1) + (i & 3)), 0, 0, 0, 0);
           }
         } else {
-          value_tile_bits(p, sh, unit_pages, page0, tile, warp, lane);
+          value_block_bits<LUT>(p, sh, pg, block, warp, sh.v_meta[t & 1][warp], tile, lane);
         }
       } else {
         value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, p.n_w + w.tok0,
@@ -858,7 +973,6 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
   return true;
 }
 
-// Softmax of stream q (warps 0..3 of its group, a thread per row), and the rows' results.
 // What a step's products need besides the weights: its value tile, and the key tile of the stream's next step
 // (`ahead` tiles on, if the piece has it).  One thread of the stream waits before it reports its weights.
 template <int KS>
@@ -869,9 +983,10 @@ __device__ __forceinline__ bool operands_ready(const ChunkParams& p, Shared& sh,
   return next >= end || wait(p, &sh.k_full[next % KS], (next / KS) & 1);
 }
 
-template <bool FRAG, int KS>
-__device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint8_t* exchange,
-                                             uint32_t tmem, int64_t g_begin, int64_t g_end, int q, int warp, int lane) {
+template <bool FRAG, bool ROPE>
+__device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sq_lo,
+                                             uint8_t* exchange, uint32_t tmem, int64_t g_begin, int64_t g_end, int q, int warp, int lane) {
+  constexpr int KS = kKeyStages;
   const int r = 32 * warp + lane;
   const uint32_t my_s = tmem + 128 * q + ((uint32_t)(32 * warp) << 16), my_o = my_s + 256;
   const int hg = 1 << p.log2hg;
@@ -887,7 +1002,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     {
       const int first = w.dual ? 64 * q : 128 * q, count = w.dual ? 64 : 128;
       for (int task = warp; task < count / 8; task += 4) {
-        const int row = first + 8 * task + (lane >> 2), c = lane & 3;
+        const int row = first + 8 * task + (lane & 7), c = lane >> 3;
         uint4 v[4] = {};
         if (row < w.rows) {
           const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.tok0 + (row >> p.log2hg);
@@ -903,6 +1018,21 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
           for (int i = 0; i < 4; ++i)
             sts16(tile + tc::chunk_offset(c >> 1, row & 127, 4 * (c & 1) + i), v[i].x, v[i].y, v[i].z, v[i].w);
         }
+      }
+    }
+    if constexpr (ROPE) {  // the low tile's queries: columns j and 8 + j are the channels of the pair at place j
+      const uint2 place = low_places(p, p.pages + w.x.unit * p.unit_page_stride, p.wk + w.x.unit * p.win_unit_stride,
+                                     p.k_new + w.x.unit * p.n * kD, lane);
+      const int row = w.dual ? r : 128 * q + r;
+      const bool mine = !w.dual || (r >> 6) == q;
+      const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.tok0 + (row >> p.log2hg);
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i) {
+        const uint32_t j = __shfl_sync(0xffffffffu, i & 1 ? place.y : place.x, i >> 1);
+        if (j == 255u || !mine) continue;
+        const uint32_t tile = sq_lo + (row >> 7) * tc::kTile16Bytes;
+        sts2(tile + tc::offset16(row & 127, j), row < w.rows ? p.q[src_row * kD + i] : (uint16_t)0);
+        sts2(tile + tc::offset16(row & 127, 8 + j), row < w.rows ? p.q[src_row * kD + 64 + i] : (uint16_t)0);
       }
     }
     fence_proxy_async_smem();
@@ -1104,17 +1234,17 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
   return true;
 }
 
-// BK, BV: code widths of fragment-order pages, or 0 for bitstream pages (widths at run time).
-template <int BK, int BV, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+// BK, BV: code widths of fragment-order pages, or 0 for bitstream pages (widths at run time; LUT: codebook levels).
+template <int BK, int BV, bool ROPE, bool LUT>
+__global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
   uint8_t* const base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sq = smem_u32(base), sk = sq + 2 * tc::kTileBytes;
-  const uint32_t sv = sk + kKeyStages<ROPE> * kKeyBytes<ROPE>;
+  const uint32_t sv = sk + kKeyStages * kKeyBytes<ROPE>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
-  constexpr int kIssuer = 8 + 2 * kProducers;
+  constexpr int kIssuer = kThreads<ROPE> / 32 - 1;
   const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
   const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
 
@@ -1135,6 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     mbar_init(&sh.v_sync, kProducers * 32);
     fence_mbar_init();
   }
+  if (ROPE && tid < kD / 2) sh.turns[tid] = p.rope_turns[tid];
   if (tid < 16) {
     sh.k_lev[tid] = p.k_lev[tid];
     sh.v_lev[tid] = p.v_lev[tid];
@@ -1152,12 +1283,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
   bool ok = true;
   if (warp < 8) {
-    ok = softmax_role<BK != 0, kKeyStages<ROPE>>(p, sh, sq, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
+    ok = softmax_role<BK != 0, ROPE>(p, sh, sq, sv + kValueStages * tc::kTileBytes, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
   } else if (warp < kIssuer) {
-    // keys on warp schedulers 0 and 1, values on 2 and 3: fewer different loops per instruction cache
-    const int block = ((warp - 8) >> 2) * 2 + (warp & 1);
-    if (warp & 2) ok = value_role<BV>(p, sh, sv, g_begin, g_end, block, lane);
-    else ok = key_role<BK, ROPE>(p, sh, sk, g_begin, g_end, block, lane);
+    const int i = warp - 8;
+    if constexpr (BK != 0) {
+      // expanding fragment-order pages, keys on warp schedulers 0 and 1 and values on 2 and 3: fewer different
+      // loops per instruction cache
+      const int block = (i >> 2) * 2 + (i & 1);
+      if (i & 2) ok = value_role<BV, LUT>(p, sh, sv, g_begin, g_end, block, lane);
+      else ok = key_role<BK, ROPE, LUT>(p, sh, sk, g_begin, g_end, 0, block, lane);
+    } else if (i < kProducers) {
+      ok = value_role<BV, LUT>(p, sh, sv, g_begin, g_end, i, lane);
+    } else {
+      ok = key_role<BK, ROPE, LUT>(p, sh, sk, g_begin, g_end, i / kProducers - 1, i % kProducers, lane);
+    }
   } else {
     ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, g_begin, g_end);
   }
@@ -1214,12 +1353,12 @@ static_assert(sizeof(Piece) <= kFirstBytes, "a CTA's place in the work list");
 // Rows of a partial slot: a job's.
 int64_t slot_rows(int64_t n, int hg) { return n >= 2 * kRows / hg ? 2 * kRows : n * hg; }
 
-template <int BK, int BV, bool ROPE>
+template <int BK, int BV, bool ROPE, bool LUT>
 cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStream_t s) {
   constexpr size_t smem = kSmemBytes<ROPE>;
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<BK, BV, ROPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<BK, BV, ROPE, LUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  chunk_kernel<BK, BV, ROPE><<<(unsigned)grid, kThreads, smem, s>>>(p);
+  chunk_kernel<BK, BV, ROPE, LUT><<<(unsigned)grid, kThreads<ROPE>, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
@@ -1265,12 +1404,14 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + sm_count * kFirstBytes);
   p.part_ml = p.part_acc + 2 * (int64_t)sm_count * p.rows_max * kD;
   if (p.lay.frag) {
-    if (p.bk == 2 && p.bv == 2) return launch_t<2, 2, false>(p, grid, launches, s);
-    if (p.bk == 4 && p.bv == 2) return launch_t<4, 2, false>(p, grid, launches, s);
-    if (p.bk == 4 && p.bv == 4) return launch_t<4, 4, false>(p, grid, launches, s);
+    if (p.bk == 2 && p.bv == 2) return launch_t<2, 2, false, false>(p, grid, launches, s);
+    if (p.bk == 4 && p.bv == 2) return launch_t<4, 2, false, false>(p, grid, launches, s);
+    if (p.bk == 4 && p.bv == 4) return launch_t<4, 4, false, false>(p, grid, launches, s);
     return cudaErrorInvalidValue;
   }
-  return rope ? launch_t<0, 0, true>(p, grid, launches, s) : launch_t<0, 0, false>(p, grid, launches, s);
+  if (p.lut)
+    return rope ? launch_t<0, 0, true, true>(p, grid, launches, s) : launch_t<0, 0, false, true>(p, grid, launches, s);
+  return rope ? launch_t<0, 0, true, false>(p, grid, launches, s) : launch_t<0, 0, false, false>(p, grid, launches, s);
 }
 
 }  // namespace kvq

@@ -64,6 +64,17 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
          ((uint64_t)2 << 61);
 }
 
+// The same for a [rows][16 fp16] tile without swizzle: groups of eight rows of 256 bytes, in each the rows' first
+// 16 bytes, then their second.
+__device__ __forceinline__ uint64_t descriptor16(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) |
+         ((uint64_t)1 << 46);
+}
+constexpr int kTile16Bytes = 128 * 32;
+__device__ __forceinline__ uint32_t offset16(int row, int col) {
+  return (uint32_t)((row >> 3) * 256 + (col >> 3) * 128 + (row & 7) * 16 + (col & 7) * 2);
+}
+
 // Instruction descriptor: fp16 x fp16 -> fp32, both operands K-major, M = 128, N columns.
 __host__ __device__ constexpr uint32_t instruction(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
