@@ -1065,57 +1065,56 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         continue;
       }
       const bool masked = __any_sync(0xffffffffu, limit < kTile);
-      float mx = -INFINITY;
+      const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
 #pragma unroll 1
-      for (int col = 0; col < kTile; col += 32) {
-        uint32_t v[32];
+      for (int col = 0; col < kTile; col += 32) {  // one pass: S is read once
+        uint32_t v[32], wt[16];
         tc::ld32(my_s + col, v);
         tc::wait_ld();
         tc::tie32(v);
         if (masked) {  // hidden columns to -inf, whatever they hold
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = col + k < limit ? v[k] : 0xFF800000u;
-          tc::st32(my_s + col, v);
         }
-        float m1 = -INFINITY;
+        float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
-          mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
           m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
         }
-        mx = fmaxf(mx, m1);
-      }
-      if (masked) tc::wait_st();
-      const float ms = mx * p.scale_log2;
-      const bool renew = ms > m_run + kLazy;  // also from -inf
-      if (__any_sync(0xffffffffu, renew)) {
-        const float factor = renew ? ex2(m_run - ms) : 1.0f;
-        if (renew) m_run = ms;
-        float lo, hi;
-        unpack2(sum2, lo, hi);
-        sum2 = pack2(lo * factor, hi * factor);
-        // the stream's product before finished with the S that was just read (they were committed together)
-        if (i > 0) {
+        const float ms = fmaxf(m0, m1) * p.scale_log2;
+        const bool renew = ms > m_run + kLazy;  // also from -inf
+        if (__any_sync(0xffffffffu, renew)) {
+          // rare: a higher maximum.  It is a whole number, so what was summed and stored moves by a power of two:
+          // l, the tile's weights so far, and O, whose last product finished with this S (they were committed
+          // together).
+          const float m_new = renew ? ceilf(ms) : m_run;
+          const float factor = renew ? ex2(m_run - m_new) : 1.0f;
+          m_run = m_new;
+          unpack2(sum2, m0, m1);
+          sum2 = pack2(m0 * factor, m1 * factor);
+          const __half2 f2 = __float2half2_rn(factor);
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t o[32];
-            tc::ld32(my_o + c, o);
-            tc::wait_ld();
-            tc::tie32(o);
+          for (int c = 0; c < col / 2; c += 16) {
+            tc::ld16(my_s + c, wt);
+            tc::wait_ld16(wt);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
-            tc::st32(my_o + c, o);
+            for (int k = 0; k < 16; ++k) wt[k] = u32(__hmul2(h2(wt[k]), f2));
+            tc::st16(my_s + c, wt);
+          }
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              tc::ld16(my_o + c, wt);
+              tc::wait_ld16(wt);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) wt[k] = __float_as_uint(__uint_as_float(wt[k]) * factor);
+              tc::st16(my_o + c, wt);
+            }
           }
         }
-      }
-      const float shift = kWeightExp - (m_run == -INFINITY ? 0.0f : m_run);
-      const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(shift, shift);
-#pragma unroll 1
-      for (int col = 0; col < kTile; col += 32) {
-        uint32_t v[32], wt[16];
-        tc::ld32(my_s + col, v);
-        tc::wait_ld();
-        tc::tie32(v);
+        const float shift = kWeightExp - (m_run == -INFINITY ? 0.0f : m_run);
+        const uint64_t shift2 = pack2(shift, shift);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           float a, c;
