@@ -170,24 +170,33 @@ __device__ __forceinline__ void load_codes(const uint8_t* codes, int block, int 
 // (column 64 (i/8) + 16 t + 8 ((i/4) % 2) + 2 (i % 4) + {0, 1}; the queries are stored in the same order), so every
 // store is 16 bytes and eight neighbouring lanes hit all banks.  Key rows take the token order
 // 16a + 8b + 2t' + e -> 8t' + 4a + 2b + e that the value block's words come in.  meta: the group's 128
-// zero point / step words in shared memory.
+// zero point / step words in shared memory (rewritten).
 //
 // The loop over the channels is kept a loop (the words are shifted along as it goes): the five roles of a
 // CTA run different code side by side, and unrolled bodies miss the instruction caches -- the unrolled
 // form of this kernel spent 4.6 of 13.6 cycles per issued instruction waiting for instructions.
 template <int B>
-__device__ __forceinline__ void key_block(uint32_t (&w)[4 * B], const uint2* meta, const __half2* mu, int slot,
-                                          uint32_t tile, int lane) {
+__device__ __forceinline__ void key_block(uint32_t (&w)[4 * B], uint2* meta, const __half2* mu, int slot, uint32_t tile,
+                                          int lane) {
   const int g = lane >> 2, t = lane & 3;
+  // once per block: (z - mu, s) of the 64 channel pairs, in the order the lanes want them
+  {
+    uint2 m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) m[h] = meta[lane + 32 * h];
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pair = lane + 32 * h;  // 4 (4q + k) + t -> 4 (4q + t) + k
+      const __half2 z = __hsub2(h2(__byte_perm(m[h].x, m[h].y, 0x5410)), mu[pair]);
+      meta[(pair & ~15) | ((pair & 3) << 2) | ((pair >> 2) & 3)] = make_uint2(u32(z), __byte_perm(m[h].x, m[h].y, 0x7632));
+    }
+    __syncwarp();
+  }
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {  // 32 channels: i = 4q .. 4q + 3
-    __half2 z[4], s[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint2 m = meta[4 * (4 * q + k) + t];
-      z[k] = __hsub2(h2(__byte_perm(m.x, m.y, 0x5410)), mu[4 * (4 * q + k) + t]);
-      s[k] = h2(__byte_perm(m.x, m.y, 0x7632));
-    }
+    const uint4 za = *reinterpret_cast<const uint4*>(meta + 4 * (4 * q + t)), zb = *reinterpret_cast<const uint4*>(meta + 4 * (4 * q + t) + 2);
+    const __half2 z[4] = {h2(za.x), h2(za.z), h2(zb.x), h2(zb.z)}, s[4] = {h2(za.y), h2(za.w), h2(zb.y), h2(zb.w)};
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -212,24 +221,31 @@ __device__ __forceinline__ void key_block(uint32_t (&w)[4 * B], const uint2* met
 
 // Values of a 32-token block of a fragment-order page, for one warp: the tile is [channel][token], and
 // a lane's words hold the token pairs that make 16 bytes of a channel's row.  meta: the block's
-// [32 tokens][D/G] zero point / step words in shared memory; half = 1 when G = 64.
+// [32 tokens][D/G] zero point / step words in 512 bytes of shared memory (rewritten); half = 1 when G = 64.
 template <int B>
-__device__ __forceinline__ void value_block(uint32_t (&w)[4 * B], const uint32_t* meta, int half, int slot,
-                                            uint32_t tile, int lane) {
+__device__ __forceinline__ void value_block(uint32_t (&w)[4 * B], uint32_t* meta, int half, int slot, uint32_t tile,
+                                            int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int per_token = 4 >> half;
+  // once per block: (z, s) of the 16 token pairs for each 32 channels, in the order the lanes want them
+  uint2* prep = reinterpret_cast<uint2*>(meta);
+  {
+    uint2 m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h, q = i >> 4, tt = (i >> 2) & 3, tok = 16 * ((i >> 1) & 1) + 8 * (i & 1) + 2 * tt;
+      const uint32_t* at = meta + tok * (4 >> half) + (q >> half);
+      const uint32_t m0 = at[0], m1 = at[4 >> half];
+      m[h] = make_uint2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) prep[lane + 32 * h] = m[h];  // [q][t][a][b]
+    __syncwarp();
+  }
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {  // channels 32q .. 32q + 31
-    __half2 z[2][2], s[2][2];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t* m = meta + (16 * a + 8 * b + 2 * t) * per_token + (q >> half);
-        const uint32_t m0 = m[0], m1 = m[per_token];
-        z[a][b] = h2(__byte_perm(m0, m1, 0x5410));
-        s[a][b] = h2(__byte_perm(m0, m1, 0x7632));
-      }
+    const uint4 za = *reinterpret_cast<const uint4*>(prep + 4 * (4 * q + t)), zb = *reinterpret_cast<const uint4*>(prep + 4 * (4 * q + t) + 2);
+    const __half2 z[2][2] = {{h2(za.x), h2(za.z)}, {h2(zb.x), h2(zb.z)}}, s[2][2] = {{h2(za.y), h2(za.w)}, {h2(zb.y), h2(zb.w)}};
 #pragma unroll
     for (int x = 0; x < 2; ++x)  // channels 16 (2q + x) + 8r + g: pair 2q + x of word r
 #pragma unroll
@@ -796,6 +812,13 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
   return true;
 }
 
+// Of a piece's tiles, how many hold page `in_tile` of a tile: they are the first ones.
+__device__ __forceinline__ int pages_of_warp(const ChunkParams& p, int64_t t_begin, int count, int in_tile) {
+  if (in_tile >= p.pages_per_tile) return 0;
+  const int64_t n = (p.n_pages - in_tile + p.pages_per_tile - 1) / p.pages_per_tile - t_begin;
+  return (int)(n < 0 ? 0 : n < count ? n : count);
+}
+
 // Key producers: warp 0..3 of a set.
 template <int BK, bool ROPE, bool LUT>
 __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int64_t g_begin, int64_t g_end,
@@ -835,58 +858,59 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
     // the next tile's meta words are on their way to shared memory, and its codes to registers (fragment order) or L2
     constexpr int NW = FRAG ? 4 * BK : 1;
     uint32_t next[NW];
-    auto page_of = [&](int64_t t) -> const uint8_t* {
-      const int64_t page = t * p.pages_per_tile + in_tile;
-      return in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages ? unit_pages + page * p.lay.bytes : nullptr;
-    };
-    auto fetch = [&](int64_t t) {
-      if (const uint8_t* pg = page_of(t)) {
+    const int count = (int)w.tiles(), first = SETS == 1 ? 0 : (int)((kt0 ^ (uint32_t)set) & 1);  // this set's first tile
+    // tiles of the piece whose page of this warp exists, and that page in tile `first`
+    const int paged = pages_of_warp(p, w.t_begin, count, in_tile);
+    const uint8_t* pg = unit_pages + ((w.t_begin + first) * p.pages_per_tile + in_tile) * p.lay.bytes;
+    const int64_t stride = (int64_t)SETS * p.pages_per_tile * p.lay.bytes;
+    const int meta_at = p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane;
+    auto fetch = [&](int i, const uint8_t* page) {
+      if (i < paged) {
         if constexpr (FRAG) {
-          load_codes<BK>(pg + p.lay.off_kc, block, lane, next);
+          load_codes<BK>(page + p.lay.off_kc, block, lane, next);
         } else if (128 * lane < 512 * p.bk) {  // the block's 512 * bits bytes
-          prefetch_l2(pg + p.lay.off_kc + block * 512 * p.bk + 128 * lane);
+          prefetch_l2(page + p.lay.off_kc + block * 512 * p.bk + 128 * lane);
         }
-        cp_async16(&sh.k_meta[set][(t / SETS) & 1][warp][4 * lane],
-                   pg + p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane);
+        cp_async16(&sh.k_meta[set][(i / SETS) & 1][warp][4 * lane], page + meta_at);
       }
       cp_async_commit();
     };
-    const int64_t first = w.t_begin + (SETS == 1 ? 0 : (kt0 ^ (uint32_t)set) & 1);  // this set's first tile
-    fetch(first);
-    for (int64_t t = first; t < w.t_end; t += SETS) {
-      const uint32_t kt = kt0 + (uint32_t)(t - w.t_begin), st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
+    fetch(first, pg);
+#pragma unroll 1
+    for (int i = first; i < count; i += SETS, pg += stride) {
+      const int64_t t = w.t_begin + i;
+      const uint32_t kt = kt0 + i, st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
       uint32_t codes[NW];
 #pragma unroll
-      for (int i = 0; i < NW; ++i) codes[i] = next[i];
-      fetch(t + SETS);
+      for (int k = 0; k < NW; ++k) codes[k] = next[k];
+      fetch(i + SETS, pg + stride);
       if (!wait(p, &sh.k_empty[st], ((kt / KS) & 1) ^ 1)) return false;
       if (t < p.page_tiles) {
-        const uint8_t* pg = page_of(t);
-        const uint32_t* meta = sh.k_meta[set][(t / SETS) & 1][warp];
+        uint32_t* meta = sh.k_meta[set][(i / SETS) & 1][warp];
         cp_async_wait<1>();
         __syncwarp();
         if constexpr (FRAG) {
-          if (pg) {
-            key_block<BK>(codes, reinterpret_cast<const uint2*>(meta), sh.mu, warp, tile, lane);
+          if (i < paged) {
+            key_block<BK>(codes, reinterpret_cast<uint2*>(meta), sh.mu, warp, tile, lane);
             if (p.nsp > 0) {
               __syncwarp();
               sparse_block(p, sh, pg, block, warp, tile, lane);
             }
           } else {
-            for (int i = lane; i < 32 * 16; i += 32)
-              sts16(tile + tc::chunk_offset(i >> 8, 32 * warp + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
+            for (int x = lane; x < 32 * 16; x += 32)
+              sts16(tile + tc::chunk_offset(x >> 8, 32 * warp + ((x & 255) >> 3), x & 7), 0, 0, 0, 0);
           }
         } else {
-          if (pg) {
+          if (i < paged) {
             const int64_t page = t * p.pages_per_tile + in_tile;
             key_block_bits<ROPE, LUT>(p, sh, pg, block, warp, reinterpret_cast<const uint4*>(meta),
                                       (uint32_t)(p.n_s + page * p.R + 32 * block + lane), lo_slot, tile, lane);
           } else {
-            for (int i = lane; i < 32 * 16; i += 32)
-              sts16(tile + tc::chunk_offset(i >> 8, 32 * warp + ((i & 255) >> 3), i & 7), 0, 0, 0, 0);
+            for (int x = lane; x < 32 * 16; x += 32)
+              sts16(tile + tc::chunk_offset(x >> 8, 32 * warp + ((x & 255) >> 3), x & 7), 0, 0, 0, 0);
             if constexpr (ROPE) {
-              for (int i = lane; i < 32 * 2; i += 32)
-                sts16(tile + tc::kTileBytes + 32 * 32 * warp + 16 * i, 0, 0, 0, 0);
+              for (int x = lane; x < 32 * 2; x += 32)
+                sts16(tile + tc::kTileBytes + 32 * 32 * warp + 16 * x, 0, 0, 0, 0);
             }
           }
         }
@@ -922,43 +946,43 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
     if (!meet(p, &sh.v_sync, &syncs)) return false;
     constexpr int NW = FRAG ? 4 * BV : 1;
     uint32_t next[NW];
-    auto page_of = [&](int64_t t) -> const uint8_t* {
-      const int64_t page = t * p.pages_per_tile + in_tile;
-      return in_tile < p.pages_per_tile && t < w.t_end && page < p.n_pages ? unit_pages + page * p.lay.bytes : nullptr;
-    };
-    auto fetch = [&](int64_t t) {
-      if (const uint8_t* pg = page_of(t)) {
+    const int count = (int)w.tiles(), paged = pages_of_warp(p, w.t_begin, count, in_tile);
+    const uint8_t* pg = unit_pages + (w.t_begin * p.pages_per_tile + in_tile) * p.lay.bytes;
+    const int64_t stride = (int64_t)p.pages_per_tile * p.lay.bytes;
+    const int meta_at = p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane;
+    auto fetch = [&](int i, const uint8_t* page) {
+      if (i < paged) {
         if constexpr (FRAG) {
-          load_codes<BV>(pg + p.lay.off_vc, block, lane, next);
+          load_codes<BV>(page + p.lay.off_vc, block, lane, next);
         } else if (128 * lane < 512 * p.bv) {
-          prefetch_l2(pg + p.lay.off_vc + block * 512 * p.bv + 128 * lane);
+          prefetch_l2(page + p.lay.off_vc + block * 512 * p.bv + 128 * lane);
         }
-        if (lane < (32 >> half))
-          cp_async16(&sh.v_meta[t & 1][warp][4 * lane], pg + p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane);
+        if (lane < (32 >> half)) cp_async16(&sh.v_meta[i & 1][warp][4 * lane], page + meta_at);
       }
       cp_async_commit();
     };
-    fetch(w.t_begin);
-    for (int64_t t = w.t_begin; t < w.t_end; ++t, ++kt) {
+    fetch(0, pg);
+#pragma unroll 1
+    for (int i = 0; i < count; ++i, ++kt, pg += stride) {
+      const int64_t t = w.t_begin + i;
       const uint32_t st = kt % kValueStages, tile = sv + st * tc::kTileBytes;
       uint32_t codes[NW];
 #pragma unroll
-      for (int i = 0; i < NW; ++i) codes[i] = next[i];
-      fetch(t + 1);
+      for (int k = 0; k < NW; ++k) codes[k] = next[k];
+      fetch(i + 1, pg + stride);
       if (!wait(p, &sh.v_empty[st], ((kt / kValueStages) & 1) ^ 1)) return false;
       if (t < p.page_tiles) {
-        const uint8_t* pg = page_of(t);
         cp_async_wait<1>();
         __syncwarp();
         if constexpr (FRAG) {
-          if (pg) {
-            value_block<BV>(codes, sh.v_meta[t & 1][warp], half, warp, tile, lane);
+          if (i < paged) {
+            value_block<BV>(codes, sh.v_meta[i & 1][warp], half, warp, tile, lane);
           } else {
-            for (int i = lane; i < 128 * 4; i += 32)
-              sts16(tile + tc::chunk_offset(warp >> 1, i >> 2, 4 * (warp & 1) + (i & 3)), 0, 0, 0, 0);
+            for (int x = lane; x < 128 * 4; x += 32)
+              sts16(tile + tc::chunk_offset(warp >> 1, x >> 2, 4 * (warp & 1) + (x & 3)), 0, 0, 0, 0);
           }
         } else {
-          value_block_bits<LUT>(p, sh, pg, block, warp, sh.v_meta[t & 1][warp], tile, lane);
+          value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[i & 1][warp], tile, lane);
         }
       } else {
         value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, p.n_w + w.tok0,
