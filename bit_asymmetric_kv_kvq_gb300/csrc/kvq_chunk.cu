@@ -54,10 +54,9 @@ constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O a
 constexpr int kValueStages = 2;
 constexpr int kBadSlots = 4;       // marks of non-finite values: producers run at most three jobs ahead
 
-// A place in the work list: a job, and where its tiles begin.
+// A place in the work list: a job of a unit, and a tile of the job.  (Counts of one CTA and one unit fit 32 bits.)
 struct Piece {
-  int64_t unit, job;         // job of the unit
-  int64_t job_start;         // its first tile in the flat list
+  int32_t unit, job, tile;
 };
 
 struct __align__(16) Shared {
@@ -97,28 +96,25 @@ __host__ __device__ inline int64_t f16_tiles_before(int64_t n_w, int log2_job_to
 }
 
 __device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t g) {
-  Piece x;
-  x.unit = g / p.tiles_per_unit;
-  const int64_t r = g - x.unit * p.tiles_per_unit;
+  const int64_t unit = g / p.tiles_per_unit, r = g - unit * p.tiles_per_unit;
   int64_t lo = 0, hi = p.jobs_per_unit - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
     if (mid * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, mid) <= r) lo = mid;
     else hi = mid - 1;
   }
-  x.job = lo;
-  x.job_start = x.unit * p.tiles_per_unit + lo * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, lo);
-  return x;
+  const int64_t before = lo * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, lo);
+  return Piece{(int32_t)unit, (int32_t)lo, (int32_t)(r - before)};
 }
 
-// The job at a place: its first chunk token, its tokens and its tiles.
-__device__ __forceinline__ int64_t job_tok0(const ChunkParams& p, const Piece& x) { return x.job << p.log2_job_tokens; }
-__device__ __forceinline__ int job_tokens(const ChunkParams& p, const Piece& x) {
-  const int64_t left = p.n - job_tok0(p, x), full = (int64_t)1 << p.log2_job_tokens;
+// A job's first chunk token, its tokens and its tiles.
+__device__ __forceinline__ int64_t job_tok0(const ChunkParams& p, int job) { return (int64_t)job << p.log2_job_tokens; }
+__device__ __forceinline__ int job_tokens(const ChunkParams& p, int job) {
+  const int64_t left = p.n - job_tok0(p, job), full = (int64_t)1 << p.log2_job_tokens;
   return (int)(left < full ? left : full);
 }
-__device__ __forceinline__ int64_t job_tiles(const ChunkParams& p, const Piece& x) {
-  return p.page_tiles + ((p.n_w + job_tok0(p, x) + job_tokens(p, x) + 127) >> 7);
+__device__ __forceinline__ int job_tiles(const ChunkParams& p, int job) {
+  return (int)(p.page_tiles + ((p.n_w + job_tok0(p, job) + job_tokens(p, job) + 127) >> 7));
 }
 
 // ------------------------------------------------------------ operand tiles
@@ -680,31 +676,34 @@ template <bool ROPE>
 constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
 static_assert(kKeyBytes<true> % 1024 == 0 && kKeySets<true> == kKeyStages, "a set of key producers per stage");
 
-// A CTA's walk over its pieces of the work list: what every role needs to know of one.
+// A CTA's walk over its pieces of the work list: `count` tiles from tile t_begin of one job of one unit.
 struct Walk {
-  Piece x;
-  int64_t tok0, job_tiles_;  // first chunk token of the job, its tiles
-  int64_t t_begin, t_end;    // tiles of the job in this piece
-  int tokens, rows;          // chunk tokens and query rows of the job
-  bool dual;                 // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
-  __device__ __forceinline__ explicit Walk(const Piece& first) : x(first) {}
-  __device__ __forceinline__ void at(const ChunkParams& p, int64_t g, int64_t g_end) {
-    tok0 = job_tok0(p, x);
-    tokens = job_tokens(p, x);
-    job_tiles_ = job_tiles(p, x);
-    t_begin = g - x.job_start;
-    const int64_t left = t_begin + (g_end - g);
-    t_end = job_tiles_ < left ? job_tiles_ : left;
+  int32_t unit, job, t_begin, count;
+  int32_t left;          // tiles of the CTA from this piece on
+  int32_t tokens, rows;  // chunk tokens and query rows of the job
+  bool dual;             // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
+  __device__ __forceinline__ Walk(const ChunkParams& p, const Piece& first, int32_t tiles)
+      : unit(first.unit), job(first.job), t_begin(first.tile), left(tiles) {
+    at(p);
+  }
+  __device__ __forceinline__ void at(const ChunkParams& p) {
+    tokens = job_tokens(p, job);
+    const int whole = job_tiles(p, job) - t_begin;
+    count = whole < left ? whole : left;
     rows = tokens << p.log2hg;
     dual = rows <= kRows;
   }
-  __device__ __forceinline__ int64_t tiles() const { return t_end - t_begin; }
-  __device__ __forceinline__ void next(const ChunkParams& p) {  // the job behind (used when a piece ends its job)
-    x.job_start += job_tiles_;
-    if (++x.job == p.jobs_per_unit) {
-      x.job = 0;
-      ++x.unit;
+  __device__ __forceinline__ int64_t tok0(const ChunkParams& p) const { return job_tok0(p, job); }
+  // Whether the piece is all of its job.
+  __device__ __forceinline__ bool whole(const ChunkParams& p) const { return t_begin == 0 && count == job_tiles(p, job); }
+  __device__ __forceinline__ void next(const ChunkParams& p) {
+    left -= count;
+    t_begin = 0;
+    if (++job == p.jobs_per_unit) {
+      job = 0;
+      ++unit;
     }
+    at(p);
   }
 };
 
@@ -759,19 +758,16 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint64_t v, 
 // products is their idle time.  The softmax streams watch the operand tiles for it (see operands_ready).
 template <bool ROPE>
 __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sk, uint32_t sv,
-                                           uint32_t tmem_, int64_t g_begin, int64_t g_end) {
+                                           uint32_t tmem_, int32_t tiles_of_cta) {
   constexpr int KS = kKeyStages;
   const bool leader = tc::elect();
   const uint32_t tmem = uniform(tmem_);
   const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv);
   const uint64_t dq_lo = tc::descriptor16(sv + kValueStages * tc::kTileBytes), dk_lo = tc::descriptor16(sk + tc::kTileBytes);
   uint32_t kt = 0, vt = 0, jobs = 0, used0 = 0, used1 = 0;  // key and value tiles, pieces, steps of the streams so far
-  Walk w(sh.first);
-  bool more = g_begin < g_end;
-  for (int64_t g = g_begin; uniform(more); w.next(p)) {
-    w.at(p, g, g_end);
+  for (Walk w(p, sh.first, tiles_of_cta); uniform(w.left) > 0; w.next(p)) {
     const bool dual = uniform(w.dual);
-    const int tiles = (int)uniform((uint32_t)w.tiles()), steps = dual ? tiles : 2 * tiles;
+    const int tiles = (int)uniform(w.count), steps = dual ? tiles : 2 * tiles;
     if (!wait(p, &sh.q_full[0], jobs & 1) || !wait(p, &sh.q_full[1], jobs & 1)) return false;
     ++jobs;
 #pragma unroll 1
@@ -806,8 +802,6 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
         kt += s + 2 < steps ? 1 : 0;
       }
     }
-    g += tiles;
-    more = g < g_end;
   }
   return true;
 }
@@ -821,20 +815,18 @@ __device__ __forceinline__ int pages_of_warp(const ChunkParams& p, int64_t t_beg
 
 // Key producers: warp 0..3 of a set.
 template <int BK, bool ROPE, bool LUT>
-__device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int64_t g_begin, int64_t g_end,
+__device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int32_t tiles_of_cta,
                                          int set, int warp, int lane) {
   constexpr bool FRAG = BK != 0;
   constexpr int KS = kKeyStages, SETS = kKeySets<ROPE>;
-  const int tid = 32 * warp + lane;
+  const int tid = 32 * (kProducers * set + warp) + lane;
   uint32_t kt0 = 0, syncs = 0;
   // the warp's 32-token block: its page of a tile and its place in the page
   const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32;
-  Walk w(sh.first);
-  for (int64_t g = g_begin; g < g_end; w.next(p)) {
-    w.at(p, g, g_end);
-    const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
-    const uint16_t* rows = p.wk + w.x.unit * p.win_unit_stride;
-    const uint16_t* fresh = p.k_new + w.x.unit * p.n * kD;
+  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; w.next(p)) {
+    const uint8_t* unit_pages = p.pages + w.unit * p.unit_page_stride;
+    const uint16_t* rows = p.wk + w.unit * p.win_unit_stride;
+    const uint16_t* fresh = p.k_new + w.unit * p.n * kD;
     uint8_t* lo_slot = sh.lo_slot[set][warp];
     if constexpr (ROPE) {
       const uint2 place = low_places(p, unit_pages, rows, fresh, lane);
@@ -845,23 +837,23 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
     } else {  // mu: the centre of each channel's range in one page of the unit
       if (!meet(p, &sh.k_sync, &syncs)) return false;  // the last piece's tiles no longer need the old one
       float mu = 0.0f;
-      if (p.n_pages > 0) {
+      if (p.n_pages > 0 && tid < kD) {
         const uint8_t* pg = unit_pages + (p.n_pages / 2) * p.lay.bytes;
         const __half2 m = h2(reinterpret_cast<const uint32_t*>(pg + p.lay.off_km)[tid]);
         const float range = __high2float(m) * (float)((1 << p.bk) - 1);
         const float centre = __low2float(m) + 0.5f * range;
         if (fabsf(centre) > range && fabsf(centre) <= 4096.0f) mu = centre;
       }
-      reinterpret_cast<__half*>(sh.mu)[tid] = __float2half_rn(mu);
+      if (tid < kD) reinterpret_cast<__half*>(sh.mu)[tid] = __float2half_rn(mu);
       if (!meet(p, &sh.k_sync, &syncs)) return false;
     }
     // the next tile's meta words are on their way to shared memory, and its codes to registers (fragment order) or L2
     constexpr int NW = FRAG ? 4 * BK : 1;
     uint32_t next[NW];
-    const int count = (int)w.tiles(), first = SETS == 1 ? 0 : (int)((kt0 ^ (uint32_t)set) & 1);  // this set's first tile
+    const int count = w.count, first = SETS == 1 ? 0 : (int)((kt0 ^ (uint32_t)set) & 1);  // this set's first tile
     // tiles of the piece whose page of this warp exists, and that page in tile `first`
     const int paged = pages_of_warp(p, w.t_begin, count, in_tile);
-    const uint8_t* pg = unit_pages + ((w.t_begin + first) * p.pages_per_tile + in_tile) * p.lay.bytes;
+    const uint8_t* pg = unit_pages + (int64_t)((w.t_begin + first) * p.pages_per_tile + in_tile) * p.lay.bytes;
     const int64_t stride = (int64_t)SETS * p.pages_per_tile * p.lay.bytes;
     const int meta_at = p.lay.off_km + (32 * block / p.G) * (kD * 4) + 16 * lane;
     auto fetch = [&](int i, const uint8_t* page) {
@@ -878,7 +870,7 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
     fetch(first, pg);
 #pragma unroll 1
     for (int i = first; i < count; i += SETS, pg += stride) {
-      const int64_t t = w.t_begin + i;
+      const int t = w.t_begin + i;
       const uint32_t kt = kt0 + i, st = kt % KS, tile = sk + st * kKeyBytes<ROPE>;
       uint32_t codes[NW];
 #pragma unroll
@@ -902,7 +894,7 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
           }
         } else {
           if (i < paged) {
-            const int64_t page = t * p.pages_per_tile + in_tile;
+            const int page = t * p.pages_per_tile + in_tile;
             key_block_bits<ROPE, LUT>(p, sh, pg, block, warp, reinterpret_cast<const uint4*>(meta),
                                       (uint32_t)(p.n_s + page * p.R + 32 * block + lane), lo_slot, tile, lane);
           } else {
@@ -915,39 +907,36 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
           }
         }
       } else {
-        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, lo_slot,
+        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, lo_slot,
                                  tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && (int64_t)kt != (int64_t)p.test_withhold - 1) mbar_arrive(&sh.k_full[st]);
     }
-    kt0 += (uint32_t)w.tiles();
-    g += w.tiles();
+    kt0 += (uint32_t)w.count;
   }
   return true;
 }
 
 // Value producers: warp 0..3.
 template <int BV, bool LUT>
-__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int64_t g_begin, int64_t g_end,
+__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int32_t tiles_of_cta,
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
   const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32, half = p.G == 64 ? 1 : 0;
-  Walk w(sh.first);
-  for (int64_t g = g_begin; g < g_end; ++jobs, w.next(p)) {
-    w.at(p, g, g_end);
-    const uint8_t* unit_pages = p.pages + w.x.unit * p.unit_page_stride;
-    const uint16_t* rows = p.wv + w.x.unit * p.win_unit_stride;
-    const uint16_t* fresh = p.v_new + w.x.unit * p.n * kD;
+  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; ++jobs, w.next(p)) {
+    const uint8_t* unit_pages = p.pages + w.unit * p.unit_page_stride;
+    const uint16_t* rows = p.wv + w.unit * p.win_unit_stride;
+    const uint16_t* fresh = p.v_new + w.unit * p.n * kD;
     uint32_t* bad = sh.bad[jobs % kBadSlots];
     if (warp == 0 && lane < 8) bad[lane] = 0;
     if (!meet(p, &sh.v_sync, &syncs)) return false;
     constexpr int NW = FRAG ? 4 * BV : 1;
     uint32_t next[NW];
-    const int count = (int)w.tiles(), paged = pages_of_warp(p, w.t_begin, count, in_tile);
-    const uint8_t* pg = unit_pages + (w.t_begin * p.pages_per_tile + in_tile) * p.lay.bytes;
+    const int count = w.count, paged = pages_of_warp(p, w.t_begin, count, in_tile);
+    const uint8_t* pg = unit_pages + (int64_t)(w.t_begin * p.pages_per_tile + in_tile) * p.lay.bytes;
     const int64_t stride = (int64_t)p.pages_per_tile * p.lay.bytes;
     const int meta_at = p.lay.off_vm + 32 * block * (16 >> half) + 16 * lane;
     auto fetch = [&](int i, const uint8_t* page) {
@@ -964,7 +953,7 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
     fetch(0, pg);
 #pragma unroll 1
     for (int i = 0; i < count; ++i, ++kt, pg += stride) {
-      const int64_t t = w.t_begin + i;
+      const int t = w.t_begin + i;
       const uint32_t st = kt % kValueStages, tile = sv + st * tc::kTileBytes;
       uint32_t codes[NW];
 #pragma unroll
@@ -985,14 +974,13 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
           value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[i & 1][warp], tile, lane);
         }
       } else {
-        value_tile_f16(p, bad, rows, fresh, (t - p.page_tiles) * kTile, p.n_w + w.tok0 + w.tokens, p.n_w + w.tok0,
+        value_tile_f16(p, bad, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, p.n_w + w.tok0(p),
                        tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.v_full[st]);
     }
-    g += w.tiles();
   }
   return true;
 }
@@ -1009,18 +997,16 @@ __device__ __forceinline__ bool operands_ready(const ChunkParams& p, Shared& sh,
 
 template <bool FRAG, bool ROPE>
 __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sq_lo,
-                                             uint8_t* exchange, uint32_t tmem, int64_t g_begin, int64_t g_end, int q, int warp, int lane) {
+                                             uint8_t* exchange, uint32_t tmem, int32_t tiles_of_cta, int q, int warp, int lane) {
   constexpr int KS = kKeyStages;
   const int r = 32 * warp + lane;
   const uint32_t my_s = tmem + 128 * q + ((uint32_t)(32 * warp) << 16), my_o = my_s + 256;
   const int hg = 1 << p.log2hg;
   uint32_t tiles0 = 0, done = 0, jobs = 0, finals = 0, halves = 0;  // tiles, steps, pieces, pieces with steps of this stream, exchanges so far
-  Walk w(sh.first);
-  for (int64_t g = g_begin; g < g_end; ++jobs, w.next(p)) {
-    w.at(p, g, g_end);
-    const int tiles = (int)w.tiles();
-    const int64_t b = w.x.unit / p.Hkv, kvh = w.x.unit - b * p.Hkv;
-    const int64_t head_row = b * p.Hq + kvh * hg;  // query row (token i, head h): (head_row + h) * n + tok0 + i
+  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; ++jobs, w.next(p)) {
+    const int tiles = w.count;
+    const int b = w.unit / p.Hkv, kvh = w.unit - b * p.Hkv;
+    const int64_t head_row = (int64_t)b * p.Hq + kvh * hg, tok0 = w.tok0(p);  // query row (token i, head h): (head_row + h) * n + tok0 + i
     // queries: job row = token * hg + head; channels in the key tiles' column order.  This stream's last
     // product of the piece before has finished, and with it every earlier one that read the tile.
     {
@@ -1029,7 +1015,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         const int row = first + 8 * task + (lane & 7), c = lane >> 3;
         uint4 v[4] = {};
         if (row < w.rows) {
-          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.tok0 + (row >> p.log2hg);
+          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + tok0 + (row >> p.log2hg);
           const uint4* src = reinterpret_cast<const uint4*>(p.q + src_row * kD) + 4 * c;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
@@ -1045,11 +1031,11 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
       }
     }
     if constexpr (ROPE) {  // the low tile's queries: columns j and 8 + j are the channels of the pair at place j
-      const uint2 place = low_places(p, p.pages + w.x.unit * p.unit_page_stride, p.wk + w.x.unit * p.win_unit_stride,
-                                     p.k_new + w.x.unit * p.n * kD, lane);
+      const uint2 place = low_places(p, p.pages + w.unit * p.unit_page_stride, p.wk + w.unit * p.win_unit_stride,
+                                     p.k_new + w.unit * p.n * kD, lane);
       const int row = w.dual ? r : 128 * q + r;
       const bool mine = !w.dual || (r >> 6) == q;
-      const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + w.tok0 + (row >> p.log2hg);
+      const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + tok0 + (row >> p.log2hg);
 #pragma unroll 1
       for (int i = 0; i < 64; ++i) {
         const uint32_t j = __shfl_sync(0xffffffffu, i & 1 ? place.y : place.x, i >> 1);
@@ -1063,19 +1049,19 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     mbar_arrive(&sh.q_full[q]);
 
     const int job_row = w.dual ? r : 128 * q + r;
-    const int64_t seen0 = p.n_w + w.tok0 + (job_row >> p.log2hg) + 1;  // fp16 rows this row sees
+    const int64_t seen0 = p.n_w + tok0 + (job_row >> p.log2hg) + 1;  // fp16 rows this row sees
     const bool live = job_row - lane < w.rows;
     float m_run = -INFINITY;
     uint64_t sum2 = 0;  // l in two halves
     const int steps = w.dual ? (tiles - q + 1) / 2 : tiles;
     for (int i = 0; i < steps; ++i, ++done) {
-      const int64_t t = w.t_begin + (w.dual ? 2 * i + q : i);
+      const int t = w.t_begin + (w.dual ? 2 * i + q : i);
       int limit;  // columns this row sees
       if (t < p.page_tiles) {
         const int64_t left = p.n_pages - t * p.pages_per_tile;
         limit = (int)(left < p.pages_per_tile ? left : p.pages_per_tile) * p.R;
       } else {
-        const int64_t seen = seen0 - (t - p.page_tiles) * kTile;
+        const int64_t seen = seen0 - (int64_t)(t - (int)p.page_tiles) * kTile;
         limit = (int)(seen < 0 ? 0 : seen > kTile ? kTile : seen);
       }
       if (!wait(p, &sh.s_full[q], done & 1)) return false;
@@ -1167,13 +1153,13 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     unpack2(sum2, l_run, l_half);
     l_run += l_half;
     // the row's result, or its partial when the job is cut; two streams of the same rows are joined first
-    const bool whole = w.t_begin == 0 && w.t_end == w.job_tiles_;
+    const bool whole = w.whole(p);
     const bool join = w.dual && tiles > 1;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (w.t_begin == 0 ? 1 : 0);
     float* xo = reinterpret_cast<float*>(exchange);  // [64 columns][128 rows]
     float f0 = 1.0f, f1 = 0.0f;
     const uint32_t* bad = sh.bad[jobs % kBadSlots];
-    const bool patch = whole || w.t_end > p.page_tiles
+    const bool patch = w.t_begin + w.count > p.page_tiles
                            ? (bad[0] | bad[1] | bad[2] | bad[3] | bad[4] | bad[5] | bad[6] | bad[7]) != 0
                            : false;
 #pragma unroll 1
@@ -1218,7 +1204,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         uint32_t fixed[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) fixed[k] = o[k];
-        patch_values(bad, p.v_new + (w.x.unit * p.n + w.tok0) * kD, min(job_row >> p.log2hg, w.tokens - 1), y, fixed);
+        patch_values(bad, p.v_new + (w.unit * p.n + tok0) * kD, min(job_row >> p.log2hg, w.tokens - 1), y, fixed);
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = fixed[k];
       }
@@ -1226,7 +1212,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         // column 8c + (e << 2 | i) holds channel 8c + 2i + e
         if (whole) {
           const float inv = l_run > 0.0f ? 1.0f / l_run : l_run == 0.0f ? 0.0f : l_run;
-          const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + w.tok0 + (job_row >> p.log2hg);
+          const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + tok0 + (job_row >> p.log2hg);
           uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD) + 4 * y;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1252,7 +1238,6 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     if (join && q == 0) mbar_arrive(&sh.x_read);
     tc::fence_before();  // O is read before the next piece's first product, which waits for its queries
     tiles0 += tiles;
-    g += tiles;
   }
   return true;
 }
@@ -1269,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   constexpr int kIssuer = kThreads<ROPE> / 32 - 1;
   const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
-  const int64_t g_end = min(g_begin + p.per_cta, p.total_tiles);
+  const int32_t tiles_of_cta = (int32_t)min(p.per_cta, p.total_tiles - g_begin);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -1284,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
     }
     mbar_init(&sh.x_written, kRows);
     mbar_init(&sh.x_read, kRows);
-    mbar_init(&sh.k_sync, kProducers * 32);
+    mbar_init(&sh.k_sync, kKeySets<ROPE> * kProducers * 32);
     mbar_init(&sh.v_sync, kProducers * 32);
     fence_mbar_init();
   }
@@ -1306,22 +1291,22 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
 
   bool ok = true;
   if (warp < 8) {
-    ok = softmax_role<BK != 0, ROPE>(p, sh, sq, sv + kValueStages * tc::kTileBytes, base + tc::kTileBytes, tmem, g_begin, g_end, warp >> 2, warp & 3, lane);
+    ok = softmax_role<BK != 0, ROPE>(p, sh, sq, sv + kValueStages * tc::kTileBytes, base + tc::kTileBytes, tmem, tiles_of_cta, warp >> 2, warp & 3, lane);
   } else if (warp < kIssuer) {
     const int i = warp - 8;
     if constexpr (BK != 0) {
       // expanding fragment-order pages, keys on warp schedulers 0 and 1 and values on 2 and 3: fewer different
       // loops per instruction cache
       const int block = (i >> 2) * 2 + (i & 1);
-      if (i & 2) ok = value_role<BV, LUT>(p, sh, sv, g_begin, g_end, block, lane);
-      else ok = key_role<BK, ROPE, LUT>(p, sh, sk, g_begin, g_end, 0, block, lane);
+      if (i & 2) ok = value_role<BV, LUT>(p, sh, sv, tiles_of_cta, block, lane);
+      else ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, 0, block, lane);
     } else if (i < kProducers) {
-      ok = value_role<BV, LUT>(p, sh, sv, g_begin, g_end, i, lane);
+      ok = value_role<BV, LUT>(p, sh, sv, tiles_of_cta, i, lane);
     } else {
-      ok = key_role<BK, ROPE, LUT>(p, sh, sk, g_begin, g_end, i / kProducers - 1, i % kProducers, lane);
+      ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, i / kProducers - 1, i % kProducers, lane);
     }
   } else {
-    ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, g_begin, g_end);
+    ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, tiles_of_cta);
   }
   if (!ok) report_error(p.err, kDevWaitTimeout);
   __syncwarp();
@@ -1338,11 +1323,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid
   pdl_wait();
   const int64_t cut = ((int64_t)blockIdx.x + 1) * p.per_cta;
   const Piece x = reinterpret_cast<const Piece*>(p.part_first)[blockIdx.x + 1];
-  if (x.job_start >= cut) return;              // the cut falls between two jobs
-  if (cut - p.per_cta > x.job_start) return;   // an earlier cut divides the same job
-  const int64_t c0 = blockIdx.x, c1 = (x.job_start + job_tiles(p, x) - 1) / p.per_cta;
-  const int64_t tok0 = job_tok0(p, x);
-  const int hg = 1 << p.log2hg, rows = job_tokens(p, x) << p.log2hg;
+  if (x.tile == 0) return;           // the cut falls between two jobs
+  if (p.per_cta < x.tile) return;    // an earlier cut divides the same job
+  const int64_t c0 = blockIdx.x, c1 = (cut - x.tile + job_tiles(p, x.job) - 1) / p.per_cta;
+  const int64_t tok0 = job_tok0(p, x.job);
+  const int hg = 1 << p.log2hg, rows = job_tokens(p, x.job) << p.log2hg;
   const int lane = threadIdx.x & 31;
   const int64_t b = x.unit / p.Hkv, kvh = x.unit - b * p.Hkv;
   for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kMergeThreads / 32)) {
@@ -1370,7 +1355,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid
   }
 }
 
-constexpr int64_t kFirstBytes = 32;
+constexpr int64_t kFirstBytes = 16;
 static_assert(sizeof(Piece) <= kFirstBytes, "a CTA's place in the work list");
 
 // Rows of a partial slot: a job's.
@@ -1422,6 +1407,7 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   int64_t grid = p.total_tiles < sm_count ? p.total_tiles : sm_count;
   p.per_cta = (p.total_tiles + grid - 1) / grid;
   grid = (p.total_tiles + p.per_cta - 1) / p.per_cta;
+  if (p.per_cta >= ((int64_t)1 << 31) || p.jobs_per_unit >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
   p.rows_max = (int32_t)slot_rows(p.n, hg);
   p.part_first = workspace;
   p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + sm_count * kFirstBytes);
