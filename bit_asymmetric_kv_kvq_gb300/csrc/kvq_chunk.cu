@@ -29,6 +29,7 @@
 // rounding.  Rotated keys have no such constant: they enter as hi + lo, two fp16 halves and two
 // products (22 bits).  Weights are rounded to fp16 scaled by 2^7, so a weight down to 2^-31 of the
 // maximum still counts; values z + s c are rounded once.
+#include <atomic>
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -66,7 +67,7 @@ struct __align__(16) Shared {
   uint32_t tmem;
   uint32_t bad[kBadSlots][8];  // tokens of the job with a non-finite value that some of its rows must not see
   __half2 mu[kD / 2];          // per channel pair
-  alignas(16) uint32_t k_meta[2][2][kProducers][128], v_meta[2][kProducers][128];  // zero points and steps of two tiles' blocks
+  alignas(16) uint32_t k_meta[2][2][kProducers][128], v_meta[kProducers][2][128];  // zero points and steps of two tiles' blocks
   alignas(8) uint8_t lo_slot[2][kProducers][64];  // rotated keys: a pair's place in the low tile, or 255
   alignas(16) unsigned long long turns[kD / 2];  // rotated keys: the turn per token of every pair
   float k_lev[16], v_lev[16];
@@ -572,52 +573,65 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
 // Values of an fp16 tile.  Tokens behind the job's first are hidden from some of its rows, and 0 * inf
 // or 0 * NaN would carry what they hold into those rows: non-finite values there enter the product as 0
 // and their tokens are marked, for patch_values to add them to the rows that do see them.
+// Warp w takes 64 channels (w & 1) of every second octet of tokens (w >> 1); the octets' bytes come through a ring of
+// RING kilobytes of its own in shared memory, so several are on their way without holding registers (with
+// one octet's loads ahead in registers a tile took 8,000 cycles).
+template <bool ROPE>  // next to rotated keys' tiles there is room for one place, where page tiles keep their meta words
+constexpr int kValueRing = ROPE ? 1 : 4;
+
+template <int RING>
 __device__ __forceinline__ void value_tile_f16(const ChunkParams& p, uint32_t* bad, const uint16_t* rows,
                                                const uint16_t* fresh, int64_t j0, int64_t end, int64_t job0,
-                                               uint32_t tile, int warp, int lane) {
-#pragma unroll 1
-  for (int batch = 0; batch < 4; ++batch) {
-    uint32_t x[2][8];  // two octets' loads in flight per lane
-    const int o = (warp >> 1) + 4 * batch, cp = 32 * (warp & 1) + lane;  // octets o and o + 2, channel pair
+                                               uint8_t* ring, uint32_t tile, int warp, int lane) {
+  const int cp = 32 * (warp & 1) + lane;  // channel pair
+  auto fetch = [&](int i) {
+    if (i < 8) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t j = j0 + 8 * (o + 2 * h);
-      if (j + 8 <= end && (j >= p.n_w || j + 8 <= p.n_w)) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(f16_row(rows, fresh, p.n_w, j)) + cp;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[h][i] = __ldg(src + i * (kD / 2));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[h][i] = j + i < end ? __ldg(reinterpret_cast<const uint32_t*>(f16_row(rows, fresh, p.n_w, j + i)) + cp) : 0u;
+      for (int h = 0; h < 2; ++h) {
+        const int tok = 4 * h + (lane >> 3);
+        const int64_t j = j0 + 8 * ((warp >> 1) + 2 * i) + tok;
+        const bool in = j < end;
+        const uint16_t* src = in ? f16_row(rows, fresh, p.n_w, j) + 64 * (warp & 1) + 8 * (lane & 7) : fresh;
+        cp_async16_or_zero(ring + (i % RING) * 1024 + tok * 128 + (lane & 7) * 16, src, in);
       }
     }
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int oct = o + 2 * h;
-      if (j0 + 8 * oct + 7 > job0) {
+  for (int i = 0; i < RING - 1; ++i) fetch(i);
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    fetch(i + RING - 1);
+    cp_async_wait<RING - 1>();
+    __syncwarp();
+    uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool lo = (x[h][i] & 0x7C00u) == 0x7C00u, hi = (x[h][i] & 0x7C000000u) == 0x7C000000u;
-          if (lo || hi) {
-            const int64_t rel = j0 + 8 * oct + i - job0;  // token of the job
-            if (rel > 0) {
-              x[h][i] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
-              x[h][i] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
-              atomicOr(&bad[rel >> 5], 1u << (rel & 31));
-            }
+    for (int k = 0; k < 8; ++k)
+      v[k] = reinterpret_cast<const uint32_t*>(ring + (i % RING) * 1024)[32 * k + lane];
+    const int oct = (warp >> 1) + 2 * i;
+    if (j0 + 8 * oct + 7 > job0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool lo = (v[k] & 0x7C00u) == 0x7C00u, hi = (v[k] & 0x7C000000u) == 0x7C000000u;
+        if (lo || hi) {
+          const int64_t rel = j0 + 8 * oct + k - job0;  // token of the job
+          if (rel > 0) {
+            v[k] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
+            v[k] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
+            atomicOr(&bad[rel >> 5], 1u << (rel & 31));
           }
         }
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // lanes 4..7 of every eight begin with their odd channel, so the eight rows are on different banks
-        const int odd = e ^ ((lane >> 2) & 1);
-        const uint32_t sel = odd ? 0x7632 : 0x5410;
-        sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + odd), oct & 7), __byte_perm(x[h][0], x[h][1], sel),
-              __byte_perm(x[h][2], x[h][3], sel), __byte_perm(x[h][4], x[h][5], sel), __byte_perm(x[h][6], x[h][7], sel));
-      }
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // lanes 4..7 of every eight begin with their odd channel, so the eight rows are on different banks
+      const int odd = e ^ ((lane >> 2) & 1);
+      const uint32_t sel = odd ? 0x7632 : 0x5410;
+      sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + odd), oct & 7), __byte_perm(v[0], v[1], sel),
+            __byte_perm(v[2], v[3], sel), __byte_perm(v[4], v[5], sel), __byte_perm(v[6], v[7], sel));
+    }
+    __syncwarp();  // the octet's place is free again
   }
 }
 
@@ -673,7 +687,11 @@ constexpr int kKeyStages = 2;
 template <bool ROPE>  // a rotated key tile has a low tile behind it, and so have the queries' tiles, behind all others
 constexpr int kKeyBytes = tc::kTileBytes + (ROPE ? tc::kTile16Bytes : 0);
 template <bool ROPE>
-constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
+constexpr int kRingBytes = ROPE ? 0 : kProducers * kValueRing<ROPE> * 1024;
+template <bool ROPE>
+constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes +
+                           kRingBytes<ROPE> + 1024;
+static_assert(kSmemBytes<true> + sizeof(Shared) <= 227 * 1024 && kSmemBytes<false> + sizeof(Shared) <= 227 * 1024, "shared memory");
 static_assert(kKeyBytes<true> % 1024 == 0 && kKeySets<true> == kKeyStages, "a set of key producers per stage");
 
 // A CTA's walk over its pieces of the work list: `count` tiles from tile t_begin of one job of one unit.
@@ -920,8 +938,8 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
 }
 
 // Value producers: warp 0..3.
-template <int BV, bool LUT>
-__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int32_t tiles_of_cta,
+template <int BV, bool ROPE, bool LUT>
+__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, uint8_t* ring, int32_t tiles_of_cta,
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
@@ -946,7 +964,7 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
         } else if (128 * lane < 512 * p.bv) {
           prefetch_l2(page + p.lay.off_vc + block * 512 * p.bv + 128 * lane);
         }
-        if (lane < (32 >> half)) cp_async16(&sh.v_meta[i & 1][warp][4 * lane], page + meta_at);
+        if (lane < (32 >> half)) cp_async16(&sh.v_meta[warp][i & 1][4 * lane], page + meta_at);
       }
       cp_async_commit();
     };
@@ -965,17 +983,17 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
         __syncwarp();
         if constexpr (FRAG) {
           if (i < paged) {
-            value_block<BV>(codes, sh.v_meta[i & 1][warp], half, warp, tile, lane);
+            value_block<BV>(codes, sh.v_meta[warp][i & 1], half, warp, tile, lane);
           } else {
             for (int x = lane; x < 128 * 4; x += 32)
               sts16(tile + tc::chunk_offset(warp >> 1, x >> 2, 4 * (warp & 1) + (x & 3)), 0, 0, 0, 0);
           }
         } else {
-          value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[i & 1][warp], tile, lane);
+          value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[warp][i & 1], tile, lane);
         }
       } else {
-        value_tile_f16(p, bad, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, p.n_w + w.tok0(p),
-                       tile, warp, lane);
+        value_tile_f16<kValueRing<ROPE>>(p, bad, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, p.n_w + w.tok0(p),
+                       ring, tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1250,6 +1268,7 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
   uint8_t* const base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sq = smem_u32(base), sk = sq + 2 * tc::kTileBytes;
   const uint32_t sv = sk + kKeyStages * kKeyBytes<ROPE>;
+  uint8_t* const rings = base + kSmemBytes<ROPE> - 1024 - kRingBytes<ROPE>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   constexpr int kIssuer = kThreads<ROPE> / 32 - 1;
@@ -1298,10 +1317,10 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
       // expanding fragment-order pages, keys on warp schedulers 0 and 1 and values on 2 and 3: fewer different
       // loops per instruction cache
       const int block = (i >> 2) * 2 + (i & 1);
-      if (i & 2) ok = value_role<BV, LUT>(p, sh, sv, tiles_of_cta, block, lane);
+      if (i & 2) ok = value_role<BV, ROPE, LUT>(p, sh, sv, ROPE ? reinterpret_cast<uint8_t*>(sh.v_meta[block]) : rings + block * kValueRing<ROPE> * 1024, tiles_of_cta, block, lane);
       else ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, 0, block, lane);
     } else if (i < kProducers) {
-      ok = value_role<BV, LUT>(p, sh, sv, tiles_of_cta, i, lane);
+      ok = value_role<BV, ROPE, LUT>(p, sh, sv, ROPE ? reinterpret_cast<uint8_t*>(sh.v_meta[i]) : rings + i * kValueRing<ROPE> * 1024, tiles_of_cta, i, lane);
     } else {
       ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, i / kProducers - 1, i % kProducers, lane);
     }
@@ -1364,13 +1383,22 @@ int64_t slot_rows(int64_t n, int hg) { return n >= 2 * kRows / hg ? 2 * kRows : 
 template <int BK, int BV, bool ROPE, bool LUT>
 cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStream_t s) {
   constexpr size_t smem = kSmemBytes<ROPE>;
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<BK, BV, ROPE, LUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the attribute is the device's for good: set once per device of the first 64, every time on others
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(chunk_kernel<BK, BV, ROPE, LUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   chunk_kernel<BK, BV, ROPE, LUT><<<(unsigned)grid, kThreads<ROPE>, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (grid == 1) return cudaSuccess;
+  if (grid == 1 || p.per_cta % p.tiles_per_unit == 0) return cudaSuccess;  // no cut inside a job
   cudaLaunchConfig_t cfg{};
   const int64_t by = (p.rows_max + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
   cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)by);

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import numpy as np
@@ -117,7 +118,7 @@ SIGNATURES = {
     "kvq_chunk_workspace": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
     "kvq_copy_sequences": (ctypes.c_int, [_P, _P, _P, _P]),
     "kvq_buffers": (ctypes.c_int, [_P, ctypes.POINTER(kvq_device_view)]),
-    "kvq_rope": (ctypes.c_int, [ctypes.POINTER(kvq_rope_config), ctypes.POINTER(kvq_rope_part), ctypes.c_int32,
+    "kvq_rope": (ctypes.c_int, [ctypes.POINTER(kvq_rope_config), _P, ctypes.c_int32,
                                 ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _P, ctypes.c_int64, _P]),
     "kvq_axis_quantize": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]),
@@ -134,6 +135,8 @@ KVQ_AXIS_CHANNELS = 1  # groups of G channels of one token (per-token scales)
 def lib():
     """Load libkvq.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -172,6 +175,8 @@ def _ptr(x):
 def _stream(stream, device=None):
     if stream is None:
         import torch
+        if isinstance(device, int):  # the raw handle, without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(device)
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
@@ -385,12 +390,17 @@ def make_rope_config(head_dim=128, rot_dim=None, base=10000.0, interleaved=False
                            original_context)
 
 
+_rope_part = struct.Struct("=QQqqqqqqii")  # kvq_rope_part
+assert _rope_part.size == ctypes.sizeof(kvq_rope_part)
+
+
 def kvq_rope(cfg: kvq_rope_config, parts, x_type: int, out_type: int, batch: int, n_tokens: int, positions, position0: int,
              stream=None) -> None:
-    """parts: a sequence of kvq_rope_part; positions: device int64 [batch][n_tokens] or None."""
-    arr = (kvq_rope_part * len(parts))(*parts)
-    _check(lib().kvq_rope(ctypes.byref(cfg), arr, len(parts), x_type, out_type, batch, n_tokens, _ptr(positions), position0,
-                          _stream(stream)), "kvq_rope")
+    """parts: a sequence of kvq_rope_part, or of the tuples of their fields; positions: device int64 [batch][n_tokens]
+    or None."""
+    packed = b"".join([_rope_part.pack(*q) if isinstance(q, tuple) else bytes(q) for q in parts])
+    _check(lib().kvq_rope(ctypes.byref(cfg), packed, len(parts), x_type, out_type, batch, n_tokens, _ptr(positions),
+                          position0, _stream(stream)), "kvq_rope")
 
 
 def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out_dtype=None, stream=None):
@@ -402,37 +412,54 @@ def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out
                cache takes.  An out may be its input's own memory.
     """
     import torch
-    types = {torch.float16: KVQ_TYPE_F16, torch.bfloat16: KVQ_TYPE_BF16, torch.float32: KVQ_TYPE_F32}
-    tensors = list(tensors)
-    rotate = [True] * len(tensors) if rotate is None else list(rotate)
-    if not tensors or len(rotate) != len(tensors) or (outs is not None and len(outs) != len(tensors)):
+    count = len(tensors)
+    if not count or (rotate is not None and len(rotate) != count) or (outs is not None and len(outs) != count):
         raise ValueError("need one to four tensors, and as many entries of rotate and outs")
     x0 = tensors[0]
-    if not isinstance(x0, torch.Tensor) or x0.dim() != 4:
-        raise ValueError("need tensors [B, n, H, D]")
-    B, n, D = x0.shape[0], x0.shape[1], cfg.head_dim
-    if outs is None:
-        outs = [torch.empty((B, t.shape[2], n, D), dtype=out_dtype or torch.float16, device=x0.device) for t in tensors]
-    for name, group, dtype in (("tensors", tensors, x0.dtype), ("outs", outs, outs[0].dtype)):
-        for t, x in zip(group, tensors):
-            want = (B, n, x.shape[2], D) if name == "tensors" else (B, x.shape[2], n, D)
-            if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != x0.device or t.dtype != dtype
-                    or t.dtype not in types or tuple(t.shape) != want or t.stride(-1) != 1):
-                raise ValueError(f"{name}: need CUDA tensors {want} of one device and type (fp16, bf16 or fp32) with "
-                                 f"contiguous channels, got {t.device} {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    if not isinstance(x0, torch.Tensor) or x0.dim() != 4 or not x0.is_cuda:
+        raise ValueError("need CUDA tensors [B, n, H, D]")
+    types = {torch.float16: KVQ_TYPE_F16, torch.bfloat16: KVQ_TYPE_BF16, torch.float32: KVQ_TYPE_F32}
+    dev, dtype, D = x0.device, x0.dtype, cfg.head_dim
+    B, n = x0.shape[:2]
+    odtype = outs[0].dtype if outs is not None else torch.float16 if out_dtype is None else out_dtype
+    if dtype not in types or odtype not in types:
+        raise ValueError(f"need fp16, bf16 or fp32, got {dtype} and {odtype}")
+    made, parts = [], []
+    for i, x in enumerate(tensors):
+        if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.dtype != dtype or x.device != dev:
+            raise ValueError(f"tensors: need tensors [B, n, H, {D}] of one device and type")
+        H = x.shape[2]
+        xb, xt, xh, xc = x.stride()
+        if x.shape != (B, n, H, D) or xc != 1:
+            raise ValueError(f"tensors: need ({B}, {n}, heads, {D}) with contiguous channels, got {tuple(x.shape)} strides "
+                             f"{x.stride()}")
+        if outs is None:
+            o = torch.empty((B, H, n, D), dtype=odtype, device=dev)
+            made.append(o)
+            ob, oh, ot = H * n * D, n * D, D
+        else:
+            o = outs[i]
+            if not isinstance(o, torch.Tensor) or o.dtype != odtype or o.device != dev or o.shape != (B, H, n, D) \
+                    or o.stride(3) != 1:
+                raise ValueError(f"outs: need {odtype} tensors ({B}, {H}, {n}, {D}) on {dev} with contiguous channels")
+            ob, oh, ot, _ = o.stride()
+        parts.append((x.data_ptr(), o.data_ptr(), xb, xt, xh, ob, ot, oh, H, 1 if rotate is None or rotate[i] else 0))
     pos, pos0 = None, 0
     if isinstance(positions, torch.Tensor):
-        if (positions.dtype != torch.int64 or positions.device != x0.device or tuple(positions.shape) != (B, n)
-                or not positions.is_contiguous()):
-            raise ValueError(f"positions: need a contiguous int64 tensor ({B}, {n}) on {x0.device}, or an integer")
+        if positions.dtype != torch.int64 or positions.device != dev or positions.shape != (B, n) \
+                or not positions.is_contiguous():
+            raise ValueError(f"positions: need a contiguous int64 tensor ({B}, {n}) on {dev}, or an integer")
         pos = positions
     else:
         pos0 = int(positions)
-    parts = [kvq_rope_part(x.data_ptr(), o.data_ptr(), x.stride(0), x.stride(1), x.stride(2), o.stride(0), o.stride(2),
-                           o.stride(1), x.shape[2], int(bool(r))) for x, o, r in zip(tensors, outs, rotate)]
-    with torch.cuda.device(x0.device):
-        kvq_rope(cfg, parts, types[x0.dtype], types[outs[0].dtype], B, n, pos, pos0, _stream(stream, x0.device))
-    return outs
+    index = dev.index
+    args = (cfg, parts, types[dtype], types[odtype], B, n, pos, pos0, _stream(stream, index))
+    if torch.cuda.current_device() == index:
+        kvq_rope(*args)
+    else:
+        with torch.cuda.device(index):
+            kvq_rope(*args)
+    return made if outs is None else list(outs)
 
 
 # ------------------------------------------------------------------ owner object
@@ -456,6 +483,7 @@ class KVCache:
                                residual, k_sparse, rope, rope_base, softmax_scale, sink_tokens,
                                0 if k_levels is None else 1)
         self.device = device
+        self._dims = (batch, num_kv_heads, num_q_heads, head_dim)
         self.handle = kvq_create(self.cfg, device)
         if k_levels is not None:
             kvq_set_codebooks(self.handle, k_levels, v_levels)
@@ -470,7 +498,7 @@ class KVCache:
         import torch
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if not t.is_cuda or t.dtype != torch.float16 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        if not t.is_cuda or t.dtype != torch.float16 or not t.is_contiguous() or t.shape != shape:
             raise ValueError(f"{name}: need a contiguous CUDA fp16 tensor of shape {tuple(shape)}, got "
                              f"{t.device} {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()}")
 
@@ -525,34 +553,37 @@ class KVCache:
 
     def _chunk(self, call, k, v, q, out, workspace, stream):
         import torch
-        c = self.cfg
+        B, Hkv, Hq, D = self._dims
         n = q.shape[2] if q.dim() == 4 else 0
-        self._need(k, (c.batch, c.num_kv_heads, n, c.head_dim), "k")
-        self._need(v, (c.batch, c.num_kv_heads, n, c.head_dim), "v")
-        self._need(q, (c.batch, c.num_q_heads, n, c.head_dim), "q")
+        self._need(k, (B, Hkv, n, D), "k")
+        self._need(v, (B, Hkv, n, D), "v")
+        self._need(q, (B, Hq, n, D), "q")
         if out is None:
             out = torch.empty_like(q)
-        self._need(out, (c.batch, c.num_q_heads, n, c.head_dim), "out")
+        else:
+            self._need(out, (B, Hq, n, D), "out")
         if workspace is None:
             workspace = self.chunk_workspace(n)
             if stream is not None and not isinstance(stream, int):
                 workspace.record_stream(stream)
             elif stream is not None:
                 workspace.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
-        if (not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous()):
+        elif not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
             raise ValueError("workspace: need a contiguous CUDA tensor on the cache's device")
-        call(self.handle, k, v, q, n, out, workspace, workspace.numel() * workspace.element_size(),
-             _stream(stream, self.device))
+        status = getattr(lib(), call)(self.handle, k.data_ptr(), v.data_ptr(), q.data_ptr(), n, out.data_ptr(),
+                                      workspace.data_ptr(), workspace.nbytes, _stream(stream, self.device))
+        if status != KVQ_OK:
+            raise KVQError(status, call)
         return out
 
     def chunk_attention(self, k, v, q, out=None, workspace=None, stream=None):
         """Attention of a chunk of n new tokens (k, v [B, Hkv, n, D], q [B, Hq, n, D]) over the cached tokens and,
         causally, over each other; the cache is not changed."""
-        return self._chunk(kvq_chunk_attention, k, v, q, out, workspace, stream)
+        return self._chunk("kvq_chunk_attention", k, v, q, out, workspace, stream)
 
     def chunk_step(self, k, v, q, out=None, workspace=None, stream=None):
         """chunk_attention(k, v, q), then append_chunk(k, v)."""
-        return self._chunk(kvq_chunk_step, k, v, q, out, workspace, stream)
+        return self._chunk("kvq_chunk_step", k, v, q, out, workspace, stream)
 
     def copy_sequences(self, src, index, stream=None):
         """Make sequence b of this cache a copy of sequence index[b] of src (a KVCache; may be this one), for every b;
