@@ -510,50 +510,62 @@ __device__ __forceinline__ void sparse_block(const ChunkParams& p, const Shared&
   }
 }
 
-// Source row of concatenated fp16 row j of a unit: the cache's rows, then the new tokens.
-__device__ __forceinline__ const uint16_t* f16_row(const uint16_t* rows, const uint16_t* fresh, int n_w, int64_t j) {
-  return j < n_w ? rows + j * kD : fresh + (j - n_w) * kD;
-}
+// The fp16 rows of a tile: rows j0 .. j0 + 127 of the list that is the cache's rows followed by the new tokens, as far
+// as the job's last token sees.
+struct F16Rows {
+  const uint16_t *a, *b;  // row r of the tile is at a + r * D for r < split, at b + r * D from there on
+  int split, end;         // rows from `end` on are not there
+  __device__ __forceinline__ F16Rows(const uint16_t* rows, const uint16_t* fresh, int n_w, int64_t j0, int64_t last)
+      : a(rows + j0 * kD), b(fresh + (j0 - n_w) * kD) {
+    const int64_t left = n_w - j0, n = last - j0;
+    split = (int)(left < 0 ? 0 : left < kTile ? left : kTile);
+    end = (int)(n < kTile ? n : kTile);
+  }
+  __device__ __forceinline__ const uint16_t* row(int r) const { return (r < split ? a : b) + r * kD; }
+};
 
-// Keys of an fp16 tile: rows j0 .. j0 + 127 of the list, zeros from `end` on.
+// Keys of an fp16 tile, zeros from the end of its rows on.
 template <bool FRAG, bool ROPE>
-__device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared& sh, const uint16_t* rows,
-                                             const uint16_t* fresh, int64_t j0, int64_t end, const uint8_t* lo_slot,
-                                             uint32_t tile, int warp, int lane) {
+__device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared& sh, const F16Rows& f, int64_t j0,
+                                             const uint8_t* lo_slot, uint32_t tile, int warp, int lane) {
   if constexpr (FRAG) {
+    const int q = lane >> 3;  // 32 channels of eight rows: all banks of a store
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {  // two rows' loads in flight per lane
       uint4 v[2][4] = {};
+      const int row0 = 8 * (warp + 2 * kProducers * half) + (lane & 7);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane & 7);  // eight rows: all banks of a store
-        if (j0 + row < end) {
-          const uint4* src = reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j0 + row)) + 4 * (lane >> 3);
+        const int row = row0 + 8 * kProducers * h;
+        const uint4* src = reinterpret_cast<const uint4*>(f.row(row)) + 4 * q;
+        if (row < f.end) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[h][i] = __ldg(src + i);
         }
       }
+      if (p.n_pages > 0) {  // else mu is 0
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 8 * (warp + kProducers * (2 * half + h)) + (lane & 7), q = lane >> 3;
-        uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
-        if (j0 + row < end) {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
+          if (row0 + 8 * kProducers * h < f.end) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
+            for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
+          }
         }
-        store_frag_row(tile, row, q, v[h]);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) store_frag_row(tile, row0 + 8 * kProducers * h, q, v[h]);
     }
   } else {
     const int row = 32 * warp + lane;
-    const int64_t j = j0 + row;
     // positions: the sink's rows first, the window behind the quantized tokens, then the new tokens
+    const int64_t j = j0 + row;
     const uint32_t pos = (uint32_t)(j < p.n_s ? j : j + p.Tq);
-    const uint4* src = j < end ? reinterpret_cast<const uint4*>(f16_row(rows, fresh, p.n_w, j)) : nullptr;
+    const uint4* src = reinterpret_cast<const uint4*>(f.row(row));
 #pragma unroll 2
     for (int q = 0; q < 8; ++q) {
       float x[8] = {}, y[8] = {};
-      if (src) {
+      if (row < f.end) {
         const uint4 vx = __ldg(src + q), vy = __ldg(src + 8 + q);
         const __half2 *hx = reinterpret_cast<const __half2*>(&vx), *hy = reinterpret_cast<const __half2*>(&vy);
 #pragma unroll
@@ -580,46 +592,43 @@ template <bool ROPE>  // next to rotated keys' tiles there is room for one place
 constexpr int kValueRing = ROPE ? 1 : 4;
 
 template <int RING>
-__device__ __forceinline__ void value_tile_f16(const ChunkParams& p, uint32_t* bad, const uint16_t* rows,
-                                               const uint16_t* fresh, int64_t j0, int64_t end, int64_t job0,
-                                               uint8_t* ring, uint32_t tile, int warp, int lane) {
+__device__ __forceinline__ void value_tile_f16(uint32_t* bad, const F16Rows& f, int job0, uint8_t* ring, uint32_t tile,
+                                               int warp, int lane) {
   const int cp = 32 * (warp & 1) + lane;  // channel pair
-  auto fetch = [&](int i) {
-    if (i < 8) {
+  const int tok = lane >> 3;              // this lane copies 16 bytes of tokens tok and tok + 4 of an octet
+  const uint32_t dst = smem_u32(ring) + 16 * lane;
+  int row = 8 * (warp >> 1) + tok;  // of the next octet to fetch
+  auto fetch = [&](int place) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = 4 * h + (lane >> 3);
-        const int64_t j = j0 + 8 * ((warp >> 1) + 2 * i) + tok;
-        const bool in = j < end;
-        const uint16_t* src = in ? f16_row(rows, fresh, p.n_w, j) + 64 * (warp & 1) + 8 * (lane & 7) : fresh;
-        cp_async16_or_zero(ring + (i % RING) * 1024 + tok * 128 + (lane & 7) * 16, src, in);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int r = row + 4 * h;
+      cp_async16_or_zero(dst + place * 1024 + 512 * h, f.row(r) + 64 * (warp & 1) + 8 * (lane & 7), r < f.end);
     }
     cp_async_commit();
+    row += 16;
   };
 #pragma unroll
   for (int i = 0; i < RING - 1; ++i) fetch(i);
 #pragma unroll 1
   for (int i = 0; i < 8; ++i) {
-    fetch(i + RING - 1);
+    if (i + RING - 1 < 8) fetch((i + RING - 1) % RING);
+    else cp_async_commit();
     cp_async_wait<RING - 1>();
     __syncwarp();
     uint32_t v[8];
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(ring + (i % RING) * 1024) + lane;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = reinterpret_cast<const uint32_t*>(ring + (i % RING) * 1024)[32 * k + lane];
+    for (int k = 0; k < 8; ++k) v[k] = src[32 * k];
     const int oct = (warp >> 1) + 2 * i;
-    if (j0 + 8 * oct + 7 > job0) {
+    if (8 * oct + 7 > job0) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const bool lo = (v[k] & 0x7C00u) == 0x7C00u, hi = (v[k] & 0x7C000000u) == 0x7C000000u;
-        if (lo || hi) {
-          const int64_t rel = j0 + 8 * oct + k - job0;  // token of the job
-          if (rel > 0) {
-            v[k] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
-            v[k] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
-            atomicOr(&bad[rel >> 5], 1u << (rel & 31));
-          }
+        const int rel = 8 * oct + k - job0;  // token of the job
+        if ((lo || hi) && rel > 0) {
+          v[k] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
+          v[k] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
+          atomicOr(&bad[rel >> 5], 1u << (rel & 31));
         }
       }
     }
@@ -925,8 +934,9 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
           }
         }
       } else {
-        key_tile_f16<FRAG, ROPE>(p, sh, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, lo_slot,
-                                 tile, warp, lane);
+        const int64_t j0 = (int64_t)(t - (int)p.page_tiles) * kTile;
+        const F16Rows f(rows, fresh, p.n_w, j0, p.n_w + w.tok0(p) + w.tokens);
+        key_tile_f16<FRAG, ROPE>(p, sh, f, j0, lo_slot, tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -992,8 +1002,9 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
           value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[warp][i & 1], tile, lane);
         }
       } else {
-        value_tile_f16<kValueRing<ROPE>>(p, bad, rows, fresh, (int64_t)(t - (int)p.page_tiles) * kTile, p.n_w + w.tok0(p) + w.tokens, p.n_w + w.tok0(p),
-                       ring, tile, warp, lane);
+        const int64_t j0 = (int64_t)(t - (int)p.page_tiles) * kTile, job0 = p.n_w + w.tok0(p);
+        const F16Rows f(rows, fresh, p.n_w, j0, job0 + w.tokens);
+        value_tile_f16<kValueRing<ROPE>>(bad, f, (int)(job0 - j0 < kTile ? job0 - j0 : kTile), ring, tile, warp, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
