@@ -165,7 +165,6 @@ struct CopySequencesParams {
   CopyRun run[3];
   const int32_t* index; // [n_dst] source sequence of every destination sequence (device)
   int32_t n_src, n_dst, Hkv, in_place;
-  int32_t slots;        // sequences fetched together (set by the launcher)
   int* err;
 };
 
@@ -203,7 +202,7 @@ struct ChunkParams {
 };
 
 // Launchers (return cudaGetLastError() after the launch).
-cudaError_t launch_copy_sequences(CopySequencesParams p, cudaStream_t s);
+cudaError_t launch_copy_sequences(const CopySequencesParams& p, cudaStream_t s);
 int copy_sequences_max_in_place();
 cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace, int* launches, cudaStream_t s);
 int64_t chunk_workspace_bytes(int64_t n, int hg, int sm_count);

@@ -105,74 +105,86 @@ struct Chunk {
 // Vector form: 16-byte aligned rows, head_dim and the rotated part multiples of 16.  A task is two
 // 8-channel chunks of a head: the two halves of eight pairs (half layout), or sixteen consecutive
 // channels (interleaved pairs, or channels that are only moved); both use the turns of pairs 8j..8j+7.
-template <typename TX, typename TO>
+// A thread keeps its token and its chunks and walks over the heads, so its eight turns stay in registers and an
+// address moves by a stride: with a division per task to find its place the same kernel reached 61 % of the
+// copy rate on 32768 tokens x 48 heads of bf16.
+template <typename TX, typename TO, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 turn[kMaxTileTokens * kMaxPairs];
   const int64_t tile = blockIdx.x / p.head_splits;
   const int head0 = (int)(blockIdx.x % p.head_splits) * p.heads_per_cta;
-  const int heads = min(p.heads_per_cta, p.heads - head0);
+  const int head1 = min(head0 + p.heads_per_cta, p.heads);
   const int64_t bt0 = tile << p.log2_tile;
   const int64_t total = p.batch * p.n_tokens;
   const int tokens = (int)min((int64_t)1 << p.log2_tile, total - bt0);
-  const int pairs = p.rot / 2;
+  const int pairs = p.rot / 2, chunks = p.D / 16, rot_chunks = p.rot / 16;
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int tok = i / pairs;
     turn[i] = turn_of(p, position_of(p, bt0 + tok), i - tok * pairs);
   }
   __syncthreads();
-  const int chunks = p.D / 16, rot_chunks = p.rot / 16;
-  // task order: chunk fastest, then token, then head, so a warp writes neighbouring tokens' rows of a head
-  const int tasks = heads * tokens * chunks;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < tasks; i += kThreads) {
-    const int row = i / chunks, j = i - row * chunks;
-    const int h_rel = row / tokens, tok = row - h_rel * tokens;
-    const int hall = head0 + h_rel;
-    int pi = 0;
+  // thread -> (head of a group, token, chunk), the chunk fastest: a warp writes neighbouring tokens' rows of a head
+  const int row = threadIdx.x / chunks, j = threadIdx.x - row * chunks;
+  const int tok = row & ((1 << p.log2_tile) - 1), hp = row >> p.log2_tile;
+  const int step = kThreads / (chunks << p.log2_tile);
+  if (hp >= step || tok >= tokens) return;
+  const int64_t b = (bt0 + tok) / p.n_tokens, t = (bt0 + tok) - b * p.n_tokens;
+  const bool in_rot = j < rot_chunks;
+  float2 cs[8];
 #pragma unroll
-    for (int k = 1; k < kMaxParts; ++k) pi += k < p.n_parts && hall >= p.part[k].head0 ? 1 : 0;
+  for (int k = 0; k < 8; ++k) cs[k] = in_rot ? turn[tok * pairs + 8 * j + k] : make_float2(1.0f, 0.0f);
+#pragma unroll 1
+  for (int pi = 0; pi < p.n_parts; ++pi) {
     const RopePart& part = p.part[pi];
-    const int64_t b = (bt0 + tok) / p.n_tokens, t = (bt0 + tok) - b * p.n_tokens;
-    const int h = hall - part.head0;
-    const bool turned = part.rotate && j < rot_chunks;
-    const bool halves = turned && !p.interleaved;
+    const int first = max(head0, part.head0);
+    const int last = min(head1, pi + 1 < p.n_parts ? p.part[pi + 1].head0 : p.heads);
+    const bool turned = part.rotate && in_rot, halves = HALVES && turned;
     const int ca = halves ? 8 * j : 16 * j, cb = halves ? p.rot / 2 + 8 * j : 16 * j + 8;
-    const TX* x = static_cast<const TX*>(part.x) + b * part.xb + t * part.xt + h * part.xh;
-    TO* o = static_cast<TO*>(part.out) + b * part.ob + t * part.ot + h * part.oh;
-    Chunk<TX> a, c;
-    a.load(x + ca);
-    c.load(x + cb);
-    float u[16];
+    const TX* x = static_cast<const TX*>(part.x) + b * part.xb + t * part.xt + (first + hp - part.head0) * part.xh;
+    TO* o = static_cast<TO*>(part.out) + b * part.ob + t * part.ot + (first + hp - part.head0) * part.oh;
+    const int64_t xs = step * part.xh, os = step * part.oh;
+    // a few heads' loads together, then their stores (an output may be its input's own memory, so the compiler
+    // cannot move loads over stores by itself)
+    constexpr int kTogether = sizeof(TX) == 2 ? 4 : 2;
+#pragma unroll 1
+    for (int h = first + hp; h < last; h += kTogether * step, x += kTogether * xs, o += kTogether * os) {
+      Chunk<TX> a[kTogether], c[kTogether];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      u[k] = a.get(k);
-      u[8 + k] = c.get(k);
-    }
-    if (turned) {
-      const float2* tr = turn + tok * pairs + 8 * j;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 cs = tr[k];
-        // first and second of pair k: (k, 8 + k) of the two halves, or (2k, 2k + 1)
-        const float x0 = halves ? u[k] : u[2 * k], x1 = halves ? u[8 + k] : u[2 * k + 1];
-        const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
-        if (halves) {
-          u[k] = y0;
-          u[8 + k] = y1;
-        } else {
-          u[2 * k] = y0;
-          u[2 * k + 1] = y1;
+      for (int e = 0; e < kTogether; ++e) {
+        if (h + e * step < last) {
+          a[e].load(x + e * xs + ca);
+          c[e].load(x + e * xs + cb);
         }
       }
-    }
-    Chunk<TO> oa, oc;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      oa.set(k, u[k]);
-      oc.set(k, u[8 + k]);
+      for (int e = 0; e < kTogether; ++e) {
+        if (h + e * step >= last) break;
+        float u[16];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          u[k] = a[e].get(k);
+          u[8 + k] = c[e].get(k);
+        }
+        if (turned) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // first and second of pair k: (k, 8 + k) of the two halves, or (2k, 2k + 1)
+            float &x0 = u[HALVES ? k : 2 * k], &x1 = u[HALVES ? 8 + k : 2 * k + 1];
+            const float y0 = x0 * cs[k].x - x1 * cs[k].y, y1 = x0 * cs[k].y + x1 * cs[k].x;
+            x0 = y0;
+            x1 = y1;
+          }
+        }
+        Chunk<TO> oa, oc;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          oa.set(k, u[k]);
+          oc.set(k, u[8 + k]);
+        }
+        oa.store(o + e * os + ca);
+        oc.store(o + e * os + cb);
+      }
     }
-    oa.store(o + ca);
-    oc.store(o + cb);
   }
 }
 
@@ -221,7 +233,8 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
 
 template <typename TX, typename TO>
 void launch_typed(const RopeParams& p, bool vector, unsigned grid, cudaStream_t s) {
-  if (vector) rope_vector_kernel<TX, TO><<<grid, kThreads, 0, s>>>(p);
+  if (vector && !p.interleaved) rope_vector_kernel<TX, TO, true><<<grid, kThreads, 0, s>>>(p);
+  else if (vector) rope_vector_kernel<TX, TO, false><<<grid, kThreads, 0, s>>>(p);
   else rope_scalar_kernel<TX, TO><<<grid, kThreads, 0, s>>>(p);
 }
 

@@ -239,7 +239,7 @@ kvq_status kvq_chunk_workspace(const kvq_cache* cache, int64_t n_tokens, int64_t
  *
  * The two configurations must agree in everything but batch and max_tokens, and so must the
  * codebooks (KVQ_ERR_INVALID_ARG); both caches must be on one device.  KVQ_ERR_CAPACITY when dst
- * cannot hold src's tokens; KVQ_ERR_STATE for a codebook cache without levels; KVQ_ERR_UNSUPPORTED in place beyond 14,528
+ * cannot hold src's tokens; KVQ_ERR_STATE for a codebook cache without levels; KVQ_ERR_UNSUPPORTED in place beyond 14,336
  * sequences.  The call uses both caches on this stream, and launches nothing when src is empty.
  */
 kvq_status kvq_copy_sequences(kvq_cache* dst, kvq_cache* src, const int32_t* index, void* cuda_stream);
