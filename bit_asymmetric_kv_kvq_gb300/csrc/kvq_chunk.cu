@@ -524,11 +524,29 @@ struct F16Rows {
   __device__ __forceinline__ const uint16_t* row(int r) const { return (r < split ? a : b) + r * kD; }
 };
 
+// This lane's 16-byte chunks of a warp's 32 rows of an fp16 tile, straight into the tile: row 32 warp + 2 i + lane / 16,
+// chunk lane % 16.  All sixteen are in flight at once and hold no registers (a load takes 1,700 cycles while the kernel
+// runs; with 4 KB a warp on its way a tile took 5,000).
+__device__ __forceinline__ uint32_t raw_chunk(int warp, int lane, int i) {
+  return tc::chunk_offset((lane & 15) >> 3, 32 * warp + 2 * i + (lane >> 4), lane & 7);
+}
+__device__ __forceinline__ void raw_rows(const F16Rows& f, uint32_t tile, int warp, int lane) {
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = 32 * warp + 2 * i + (lane >> 4);
+    cp_async16_or_zero(tile + raw_chunk(warp, lane, i), f.row(r) + 8 * (lane & 15), r < f.end);
+  }
+  cp_async_commit();
+  cp_async_wait_all();
+}
+
 // Keys of an fp16 tile, zeros from the end of its rows on.
 template <bool FRAG, bool ROPE>
 __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared& sh, const F16Rows& f, int64_t j0,
                                              const uint8_t* lo_slot, uint32_t tile, int warp, int lane) {
-  if constexpr (FRAG) {
+  if (!ROPE && p.page_tiles == 0) {  // no pages: mu is 0 and the columns keep their order
+    raw_rows(f, tile, warp, lane);
+  } else if constexpr (FRAG) {
     const int q = lane >> 3;  // 32 channels of eight rows: all banks of a store
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {  // two rows' loads in flight per lane
@@ -543,14 +561,12 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
           for (int i = 0; i < 4; ++i) v[h][i] = __ldg(src + i);
         }
       }
-      if (p.n_pages > 0) {  // else mu is 0
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
-          if (row0 + 8 * kProducers * h < f.end) {
+      for (int h = 0; h < 2; ++h) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(v[h]);
+        if (row0 + 8 * kProducers * h < f.end) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
-          }
+          for (int i = 0; i < 16; ++i) x[i] = u32(__hsub2(h2(x[i]), sh.mu[16 * q + i]));
         }
       }
 #pragma unroll
@@ -582,78 +598,51 @@ __device__ __forceinline__ void key_tile_f16(const ChunkParams& p, const Shared&
   }
 }
 
-// Values of an fp16 tile.  Tokens behind the job's first are hidden from some of its rows, and 0 * inf
-// or 0 * NaN would carry what they hold into those rows: non-finite values there enter the product as 0
-// and their tokens are marked, for patch_values to add them to the rows that do see them.
-// Warp w takes 64 channels (w & 1) of every second octet of tokens (w >> 1); the octets' bytes come through a ring of
-// RING kilobytes of its own in shared memory, so several are on their way without holding registers (with
-// one octet's loads ahead in registers a tile took 8,000 cycles).
-template <bool ROPE>  // next to rotated keys' tiles there is room for one place, where page tiles keep their meta words
-constexpr int kValueRing = ROPE ? 1 : 4;
-
-template <int RING>
-__device__ __forceinline__ void value_tile_f16(uint32_t* bad, const F16Rows& f, int job0, uint8_t* ring, uint32_t tile,
+// Values of an fp16 tile: token rows as they are (the product takes them MN-major); next to page tiles the channels of
+// every eight go into value_row order.  Tokens behind the job's first (row job0 of the tile) are hidden from some of its
+// rows, and 0 * inf or 0 * NaN would carry what they hold into those rows: non-finite values there enter the product as
+// 0 and their tokens are marked, for patch_values to add them to the rows that do see them.
+__device__ __forceinline__ void value_tile_f16(uint32_t* bad, const F16Rows& f, int job0, bool reorder, uint32_t tile,
                                                int warp, int lane) {
-  const int cp = 32 * (warp & 1) + lane;  // channel pair
-  const int tok = lane >> 3;              // this lane copies 16 bytes of tokens tok and tok + 4 of an octet
-  const uint32_t dst = smem_u32(ring) + 16 * lane;
-  int row = 8 * (warp >> 1) + tok;  // of the next octet to fetch
-  auto fetch = [&](int place) {
+  raw_rows(f, tile, warp, lane);
+  const bool check = 32 * warp + 31 > job0;
+  if (!reorder && !check) return;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {  // each lane the chunks it copied itself
+    const uint32_t at = tile + raw_chunk(warp, lane, i);
+    const int r = 32 * warp + 2 * i + (lane >> 4);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+    if (check && r > job0) {
+      bool any = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row + 4 * h;
-      cp_async16_or_zero(dst + place * 1024 + 512 * h, f.row(r) + 64 * (warp & 1) + 8 * (lane & 7), r < f.end);
-    }
-    cp_async_commit();
-    row += 16;
-  };
-#pragma unroll
-  for (int i = 0; i < RING - 1; ++i) fetch(i);
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    if (i + RING - 1 < 8) fetch((i + RING - 1) % RING);
-    else cp_async_commit();
-    cp_async_wait<RING - 1>();
-    __syncwarp();
-    uint32_t v[8];
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(ring + (i % RING) * 1024) + lane;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = src[32 * k];
-    const int oct = (warp >> 1) + 2 * i;
-    if (8 * oct + 7 > job0) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool lo = (v[k] & 0x7C00u) == 0x7C00u, hi = (v[k] & 0x7C000000u) == 0x7C000000u;
-        const int rel = 8 * oct + k - job0;  // token of the job
-        if ((lo || hi) && rel > 0) {
-          v[k] &= lo ? 0xFFFF0000u : 0xFFFFFFFFu;
-          v[k] &= hi ? 0x0000FFFFu : 0xFFFFFFFFu;
-          atomicOr(&bad[rel >> 5], 1u << (rel & 31));
-        }
+      for (int k = 0; k < 4; ++k) {
+        const bool lo = (w[k] & 0x7C00u) == 0x7C00u, hi = (w[k] & 0x7C000000u) == 0x7C000000u;
+        any |= lo || hi;
+        w[k] &= (lo ? 0u : 0x0000FFFFu) | (hi ? 0u : 0xFFFF0000u);
       }
+      if (any) atomicOr(&bad[(r - job0) >> 5], 1u << ((r - job0) & 31));
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      // lanes 4..7 of every eight begin with their odd channel, so the eight rows are on different banks
-      const int odd = e ^ ((lane >> 2) & 1);
-      const uint32_t sel = odd ? 0x7632 : 0x5410;
-      sts16(tile + tc::chunk_offset(oct >> 3, value_row(2 * cp + odd), oct & 7), __byte_perm(v[0], v[1], sel),
-            __byte_perm(v[2], v[3], sel), __byte_perm(v[4], v[5], sel), __byte_perm(v[6], v[7], sel));
-    }
-    __syncwarp();  // the octet's place is free again
+    if (reorder)
+      sts16(at, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+            __byte_perm(w[2], w[3], 0x7632));
+    else
+      sts16(at, w[0], w[1], w[2], w[3]);
   }
 }
 
 // What the marked tokens up to the row's own add to its channels 32y .. 32y + 31: their non-finite values
-// (every visible token has a positive weight, so inf or NaN is the sum's).  `o` is in value_row order.
-__device__ __forceinline__ void patch_values(const uint32_t* bad, const uint16_t* job_v, int token, int y, uint32_t* o) {
+// (every visible token has a positive weight, so inf or NaN is the sum's).  `o` is in value_row order if reordered.
+__device__ __forceinline__ void patch_values(const uint32_t* bad, const uint16_t* job_v, int token, int y, bool reordered,
+                                             uint32_t* o) {
 #pragma unroll 1
   for (int i = 1; i <= token; ++i) {
     if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
 #pragma unroll 1
     for (int c = 0; c < 32; ++c) {
       const float f = __half2float(__ushort_as_half(job_v[(int64_t)i * kD + 32 * y + c]));
-      if (!isfinite(f)) o[value_row(c)] = __float_as_uint(__uint_as_float(o[value_row(c)]) + f);
+      const int at = reordered ? value_row(c) : c;
+      if (!isfinite(f)) o[at] = __float_as_uint(__uint_as_float(o[at]) + f);
     }
   }
 }
@@ -696,10 +685,7 @@ constexpr int kKeyStages = 2;
 template <bool ROPE>  // a rotated key tile has a low tile behind it, and so have the queries' tiles, behind all others
 constexpr int kKeyBytes = tc::kTileBytes + (ROPE ? tc::kTile16Bytes : 0);
 template <bool ROPE>
-constexpr int kRingBytes = ROPE ? 0 : kProducers * kValueRing<ROPE> * 1024;
-template <bool ROPE>
-constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes +
-                           kRingBytes<ROPE> + 1024;
+constexpr int kSmemBytes = 2 * kKeyBytes<ROPE> + kKeyStages * kKeyBytes<ROPE> + kValueStages * tc::kTileBytes + 1024;
 static_assert(kSmemBytes<true> + sizeof(Shared) <= 227 * 1024 && kSmemBytes<false> + sizeof(Shared) <= 227 * 1024, "shared memory");
 static_assert(kKeyBytes<true> % 1024 == 0 && kKeySets<true> == kKeyStages, "a set of key producers per stage");
 
@@ -776,6 +762,12 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, uint64_t v, 
     tc::mma_ts(d, pcol + 8 * i, v + off, tc::instruction(kD), accumulate || i > 0);
   }
 }
+// The same with token rows (fp16 tiles): 16 tokens are 16 rows of 128 bytes.
+__device__ __forceinline__ void issue_pv_rows(uint32_t d, uint32_t pcol, uint64_t v, bool accumulate) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    tc::mma_ts(d, pcol + 8 * i, v + i * (2048 >> 4), tc::instruction(kD) | tc::kTransposeB, accumulate || i > 0);
+}
 
 // The issuing warp.  Step s of a piece is one stream's turn at one tile; QK runs two steps ahead of PV, so
 // between a stream's QK and its PV the tensor cores have the other stream's products.  P overlies S: QK of
@@ -789,7 +781,7 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
   constexpr int KS = kKeyStages;
   const bool leader = tc::elect();
   const uint32_t tmem = uniform(tmem_);
-  const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv);
+  const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv), dv_rows = tc::descriptor_mn(sv);
   const uint64_t dq_lo = tc::descriptor16(sv + kValueStages * tc::kTileBytes), dk_lo = tc::descriptor16(sk + tc::kTileBytes);
   uint32_t kt = 0, vt = 0, jobs = 0, used0 = 0, used1 = 0;  // key and value tiles, pieces, steps of the streams so far
   for (Walk w(p, sh.first, tiles_of_cta); uniform(w.left) > 0; w.next(p)) {
@@ -802,6 +794,7 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
       const uint32_t q = s & 1, at = 128 * q;
       const bool last = dual || q == 1;  // the tile's last step
       const uint32_t vs = vt % kValueStages, ks = kt % KS;
+      const bool paged = uniform(w.t_begin) + (dual ? s : s >> 1) < (int)p.page_tiles;  // of step s
       if (s >= 0) {  // the stream's weights, its value tile and the key tile of its next step are there
         if (!wait(p, &sh.p_ready[q], (q ? used1 : used0) & 1)) return false;
         if (q) ++used1;
@@ -812,7 +805,9 @@ __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uin
       tc::fence_after();
       if (leader) {
         if (s >= 0) {
-          issue_pv(tmem + 256 + at, tmem + at, dv + vs * (tc::kTileBytes >> 4), s >= 2);
+          const uint32_t stage = vs * (tc::kTileBytes >> 4);
+          if (paged) issue_pv(tmem + 256 + at, tmem + at, dv + stage, s >= 2);
+          else issue_pv_rows(tmem + 256 + at, tmem + at, dv_rows + stage, s >= 2);
           if (last) tc::commit(&sh.v_empty[vs]);
         }
         if (s + 2 < steps) {
@@ -949,7 +944,7 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
 
 // Value producers: warp 0..3.
 template <int BV, bool ROPE, bool LUT>
-__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, uint8_t* ring, int32_t tiles_of_cta,
+__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int32_t tiles_of_cta,
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
@@ -978,37 +973,45 @@ __device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uin
       }
       cp_async_commit();
     };
+    auto ready = [&] { return wait(p, &sh.v_empty[kt % kValueStages], ((kt / kValueStages) & 1) ^ 1); };
+    auto done = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.v_full[kt % kValueStages]);
+      ++kt;
+    };
+    int i = 0;
     fetch(0, pg);
 #pragma unroll 1
-    for (int i = 0; i < count; ++i, ++kt, pg += stride) {
-      const int t = w.t_begin + i;
-      const uint32_t st = kt % kValueStages, tile = sv + st * tc::kTileBytes;
+    for (; i < count && w.t_begin + i < (int)p.page_tiles; ++i, pg += stride) {
+      const uint32_t tile = sv + (kt % kValueStages) * tc::kTileBytes;
       uint32_t codes[NW];
 #pragma unroll
       for (int k = 0; k < NW; ++k) codes[k] = next[k];
       fetch(i + 1, pg + stride);
-      if (!wait(p, &sh.v_empty[st], ((kt / kValueStages) & 1) ^ 1)) return false;
-      if (t < p.page_tiles) {
-        cp_async_wait<1>();
-        __syncwarp();
-        if constexpr (FRAG) {
-          if (i < paged) {
-            value_block<BV>(codes, sh.v_meta[warp][i & 1], half, warp, tile, lane);
-          } else {
-            for (int x = lane; x < 128 * 4; x += 32)
-              sts16(tile + tc::chunk_offset(warp >> 1, x >> 2, 4 * (warp & 1) + (x & 3)), 0, 0, 0, 0);
-          }
+      if (!ready()) return false;
+      cp_async_wait<1>();
+      __syncwarp();
+      if constexpr (FRAG) {
+        if (i < paged) {
+          value_block<BV>(codes, sh.v_meta[warp][i & 1], half, warp, tile, lane);
         } else {
-          value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[warp][i & 1], tile, lane);
+          for (int x = lane; x < 128 * 4; x += 32)
+            sts16(tile + tc::chunk_offset(warp >> 1, x >> 2, 4 * (warp & 1) + (x & 3)), 0, 0, 0, 0);
         }
       } else {
-        const int64_t j0 = (int64_t)(t - (int)p.page_tiles) * kTile, job0 = p.n_w + w.tok0(p);
-        const F16Rows f(rows, fresh, p.n_w, j0, job0 + w.tokens);
-        value_tile_f16<kValueRing<ROPE>>(bad, f, (int)(job0 - j0 < kTile ? job0 - j0 : kTile), ring, tile, warp, lane);
+        value_block_bits<LUT>(p, sh, i < paged ? pg : nullptr, block, warp, sh.v_meta[warp][i & 1], tile, lane);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.v_full[st]);
+      done();
+    }
+#pragma unroll 1
+    for (; i < count; ++i) {  // fp16 rows
+      const int64_t j0 = (int64_t)(w.t_begin + i - (int)p.page_tiles) * kTile, job0 = p.n_w + w.tok0(p);
+      const F16Rows f(rows, fresh, p.n_w, j0, job0 + w.tokens);
+      if (!ready()) return false;
+      value_tile_f16(bad, f, (int)(job0 - j0 < kTile ? job0 - j0 : kTile), p.page_tiles > 0,
+                     sv + (kt % kValueStages) * tc::kTileBytes, warp, lane);
+      done();
     }
   }
   return true;
@@ -1050,7 +1053,7 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
           for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
         }
         const uint32_t tile = sq + (row >> 7) * tc::kTileBytes;
-        if constexpr (FRAG) {
+        if (FRAG && p.page_tiles > 0) {
           store_frag_row(tile, row & 127, c, v);
         } else {
 #pragma unroll
@@ -1233,12 +1236,15 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
         uint32_t fixed[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) fixed[k] = o[k];
-        patch_values(bad, p.v_new + (w.unit * p.n + tok0) * kD, min(job_row >> p.log2hg, w.tokens - 1), y, fixed);
+        patch_values(bad, p.v_new + (w.unit * p.n + tok0) * kD, min(job_row >> p.log2hg, w.tokens - 1), y, p.page_tiles > 0,
+                     fixed);
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = fixed[k];
       }
       if (job_row < w.rows) {
-        // column 8c + (e << 2 | i) holds channel 8c + 2i + e
+        // channel c of the 32: column value_row(c), or column c without pages
+        const bool plain = p.page_tiles == 0;
+        auto at = [&](int c) { return __uint_as_float(plain ? o[c] : o[(c & ~7) | ((c & 1) << 2) | ((c & 7) >> 1)]); };
         if (whole) {
           const float inv = l_run > 0.0f ? 1.0f / l_run : l_run == 0.0f ? 0.0f : l_run;
           const int64_t row = (head_row + (job_row & (hg - 1))) * p.n + tok0 + (job_row >> p.log2hg);
@@ -1248,17 +1254,14 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              h[k] = u32(__floats2half2_rn(__uint_as_float(o[8 * c + k]) * inv, __uint_as_float(o[8 * c + 4 + k]) * inv));
+              h[k] = u32(__floats2half2_rn(at(8 * c + 2 * k) * inv, at(8 * c + 2 * k + 1) * inv));
             dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
           }
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_acc + (slot * p.rows_max + job_row) * kD) + 8 * y;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; k += 2)
-              dst[2 * c + k / 2] = make_float4(__uint_as_float(o[8 * c + k]), __uint_as_float(o[8 * c + 4 + k]),
-                                               __uint_as_float(o[8 * c + k + 1]), __uint_as_float(o[8 * c + 5 + k]));
+          for (int c = 0; c < 8; ++c)
+            dst[c] = make_float4(at(4 * c), at(4 * c + 1), at(4 * c + 2), at(4 * c + 3));
           if (y == 0)
             *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows_max + job_row) * 2) = make_float2(m_run, l_run);
         }
@@ -1279,7 +1282,6 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
   uint8_t* const base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t sq = smem_u32(base), sk = sq + 2 * tc::kTileBytes;
   const uint32_t sv = sk + kKeyStages * kKeyBytes<ROPE>;
-  uint8_t* const rings = base + kSmemBytes<ROPE> - 1024 - kRingBytes<ROPE>;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   constexpr int kIssuer = kThreads<ROPE> / 32 - 1;
@@ -1328,10 +1330,10 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
       // expanding fragment-order pages, keys on warp schedulers 0 and 1 and values on 2 and 3: fewer different
       // loops per instruction cache
       const int block = (i >> 2) * 2 + (i & 1);
-      if (i & 2) ok = value_role<BV, ROPE, LUT>(p, sh, sv, ROPE ? reinterpret_cast<uint8_t*>(sh.v_meta[block]) : rings + block * kValueRing<ROPE> * 1024, tiles_of_cta, block, lane);
+      if (i & 2) ok = value_role<BV, ROPE, LUT>(p, sh, sv, tiles_of_cta, block, lane);
       else ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, 0, block, lane);
     } else if (i < kProducers) {
-      ok = value_role<BV, ROPE, LUT>(p, sh, sv, ROPE ? reinterpret_cast<uint8_t*>(sh.v_meta[i]) : rings + i * kValueRing<ROPE> * 1024, tiles_of_cta, i, lane);
+      ok = value_role<BV, ROPE, LUT>(p, sh, sv, tiles_of_cta, i, lane);
     } else {
       ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, i / kProducers - 1, i % kProducers, lane);
     }

@@ -75,6 +75,14 @@ __device__ __forceinline__ uint32_t offset16(int row, int col) {
   return (uint32_t)((row >> 3) * 256 + (col >> 3) * 128 + (row & 7) * 16 + (col & 7) * 2);
 }
 
+// The same block with the contraction index along the rows instead ("MN-major": 64 columns of the other operand
+// index in 128 bytes, one row per contraction index): 16384 bytes to the next 64 columns, 1024 to the next eight rows.
+__device__ __forceinline__ uint64_t descriptor_mn(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(kBlockBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kTransposeB = 1u << 16;  // in the instruction descriptor: B is MN-major
+
 // Instruction descriptor: fp16 x fp16 -> fp32, both operands K-major, M = 128, N columns.
 __host__ __device__ constexpr uint32_t instruction(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);

@@ -12,6 +12,7 @@ Two layers:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -181,6 +182,14 @@ def _stream(stream, device=None):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _allocating_on(stream, device):
+    """Context in which torch allocates for `stream` (None: the current one, nothing to do)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
 def make_config(batch, num_kv_heads, num_q_heads, head_dim, max_tokens, k_bits, v_bits, group_size, residual,
@@ -434,7 +443,11 @@ def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out
             raise ValueError(f"tensors: need ({B}, {n}, heads, {D}) with contiguous channels, got {tuple(x.shape)} strides "
                              f"{x.stride()}")
         if outs is None:
-            o = torch.empty((B, H, n, D), dtype=odtype, device=dev)
+            if stream is None:
+                o = torch.empty((B, H, n, D), dtype=odtype, device=dev)
+            else:
+                with _allocating_on(stream, dev):
+                    o = torch.empty((B, H, n, D), dtype=odtype, device=dev)
             made.append(o)
             ob, oh, ot = H * n * D, n * D, D
         else:
@@ -443,6 +456,8 @@ def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out
                     or o.stride(3) != 1:
                 raise ValueError(f"outs: need {odtype} tensors ({B}, {H}, {n}, {D}) on {dev} with contiguous channels")
             ob, oh, ot, _ = o.stride()
+            if (B > 1 and ob == 0) or (H > 1 and oh == 0) or (n > 1 and ot == 0):
+                raise ValueError("outs: several tokens or heads share memory")
         parts.append((x.data_ptr(), o.data_ptr(), xb, xt, xh, ob, ot, oh, H, 1 if rotate is None or rotate[i] else 0))
     pos, pos0 = None, 0
     if isinstance(positions, torch.Tensor):
@@ -558,17 +573,19 @@ class KVCache:
         self._need(k, (B, Hkv, n, D), "k")
         self._need(v, (B, Hkv, n, D), "v")
         self._need(q, (B, Hq, n, D), "q")
-        if out is None:
-            out = torch.empty_like(q)
+        if out is None or workspace is None:
+            # what is made here belongs to the stream that the call runs on: a block of another stream's could still
+            # be in use there
+            with _allocating_on(stream, self.device):
+                if out is None:
+                    out = torch.empty_like(q)
+                else:
+                    self._need(out, (B, Hq, n, D), "out")
+                if workspace is None:
+                    workspace = self.chunk_workspace(n)
         else:
             self._need(out, (B, Hq, n, D), "out")
-        if workspace is None:
-            workspace = self.chunk_workspace(n)
-            if stream is not None and not isinstance(stream, int):
-                workspace.record_stream(stream)
-            elif stream is not None:
-                workspace.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
-        elif not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
+        if not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
             raise ValueError("workspace: need a contiguous CUDA tensor on the cache's device")
         status = getattr(lib(), call)(self.handle, k.data_ptr(), v.data_ptr(), q.data_ptr(), n, out.data_ptr(),
                                       workspace.data_ptr(), workspace.nbytes, _stream(stream, self.device))

@@ -207,8 +207,10 @@ kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_f16, const void* v_f
  * Keys and values are expanded to fp16 for the tensor cores (keys as differences from a per-channel
  * offset that cancels in the softmax, or as a high and a low half when they are rotated), products
  * accumulate in fp32, the softmax statistics are fp32, and the weights are rounded to fp16 before
- * the value product.  Sums are taken in a fixed order: outputs are bitwise reproducible.  A cached or
- * new token that a query does not attend cannot change its output, whatever it holds.
+ * the value product.  Outputs stay within a max relative error of 2e-3 per row of exact attention over the
+ * dequantized cache and the chunk, like kvq_decode_attention's.  fp16's range is the limit: keys are finite for
+ * |k| <= 61,408 (46,000 when they are rotated).  Sums are taken in a fixed order: outputs are bitwise
+ * reproducible.  A token that a query does not attend cannot change its output, whatever it holds.
  *
  * workspace: device memory of at least kvq_chunk_workspace bytes, 16-byte aligned; it holds partial
  * results of one call, so calls that may overlap on the GPU (other streams, graphs replayed at the
@@ -457,7 +459,8 @@ kvq_status kvq_sync_status(kvq_cache* cache, void* cuda_stream);
  * leaving copies in flight; kvq_sync_status then reports KVQ_ERR_CUDA.  This hook makes that path
  * testable without a fault: for the decode launches that follow, wait_limit_ns > 0 replaces the
  * default limit, and withhold_page = k >= 0 leaves page k of every CTA's slice of the work list
- * uncopied, so the warps that reach it wait until the limit runs out.  (-1, 0) restores normal
+ * uncopied, so the warps that reach it wait until the limit runs out (chunk attention: key tile k of every CTA's
+ * part of the list is never reported ready).  (-1, 0) restores normal
  * operation.  Outputs of affected launches are not meaningful.  KVQ_ERR_INVALID_ARG for
  * withhold_page < -1 or wait_limit_ns < 0.  (The method pages have no counterpart.)
  */

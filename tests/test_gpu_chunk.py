@@ -312,6 +312,18 @@ def test_other_stream_and_captured_graph():
     got = cache.chunk_attention(kn, vn, qd, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+    got = cache.chunk_attention(kn, vn, qd, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(got, want)
+    # two caches, each with a workspace of its own, at the same time on two streams
+    other = kvq.KVCache.for_workload(w, max_tokens=T + n)
+    other.prefill_quantize(_dev(K[:, :, :T]), _dev(V[:, :, :T]))
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [c.chunk_attention(kn, vn, qd, stream=x) for _ in range(8) for c, x in ((cache, a), (other, b))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in outs)
+    other.close()
     out, ws = torch.empty_like(qd), cache.chunk_workspace(n)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -323,6 +335,35 @@ def test_other_stream_and_captured_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, cache.chunk_attention(kn, vn, _dev(q2)))
     cache.close()
+
+
+@pytest.mark.parametrize("method", ["k2v2", "k3v3rope"])
+def test_wait_runs_out_and_is_reported(method):
+    """A key tile that is never reported ready: every wait gives up after 1 ms, the call comes back, the error is
+    reported, and the context goes on working."""
+    import time
+    kvq = _kvq()
+    T, n = 900, 20
+    w = _workload(method, 1, 2, 4, T, n)
+    K, V, q = _inputs(w, T, n)
+    kn, vn, qd = _dev(K[:, :, T:]), _dev(V[:, :, T:]), _dev(q)
+    caches = [kvq.KVCache.for_workload(w, max_tokens=T + n) for _ in range(2)]
+    for c in caches:
+        c.prefill_quantize(_dev(K[:, :, :T]), _dev(V[:, :, :T]))
+        assert c.sync_status() == 0
+    kvq.kvq.kvq_test_inject(caches[0].handle, 0, 1_000_000)
+    t0 = time.perf_counter()
+    caches[0].chunk_attention(kn, vn, qd)
+    assert caches[0].sync_status() == kvq.kvq.KVQ_ERR_CUDA
+    assert time.perf_counter() - t0 < 1.0
+    with pytest.raises(kvq.KVQError):
+        caches[0].chunk_step(kn, vn, qd)
+    out = caches[1].chunk_attention(kn, vn, qd)
+    assert caches[1].sync_status() == 0
+    units = {(0, h): _unit(w, K[0, h, :T], V[0, h, :T]) for h in range(2)}
+    _check(w, units, K, V, q, out, T, T + n)
+    for c in caches:
+        c.close()
 
 
 def test_refusals():

@@ -169,6 +169,7 @@ def test_binding_refusals():
                 lambda: kvq.rope(cfg, [x], torch.zeros(1, 3, dtype=torch.int64, device="cuda")),
                 lambda: kvq.rope(cfg, [x], rotate=[True, False]), lambda: kvq.rope(cfg, [x], outs=[x]),
                 lambda: kvq.rope(cfg, [x.transpose(2, 3).contiguous().transpose(2, 3)]),
+                lambda: kvq.rope(cfg, [x], outs=[torch.zeros(1, 1, 4, 128, device="cuda").half().expand(1, 2, 4, 128)]),
                 lambda: kvq.rope(cfg, [x], out_dtype=torch.float64),
                 lambda: kvq.make_rope_config(scaling="other")):
         with pytest.raises(ValueError):
