@@ -51,13 +51,18 @@ template <bool ROPE>
 constexpr int kThreads = (8 + (kKeySets<ROPE> + 1) * kProducers + 1) * 32;
 constexpr float kLazy = 8.0f;      // log2 units the running maximum may lag behind
 constexpr float kWeightExp = 7.0f; // weights are at most 2^(8 + 7): below fp16's 65504
+// A job costs more than its tiles: its queries are fetched, the pipeline fills, its rows are written.  The cuts between
+// CTAs count that as three tiles (measured: 13,000 cycles a job, 4,000 a tile); without it a CTA with the short jobs of a
+// prompt's beginning took half as long again as the others.
+constexpr int kJobCost = 3;
 constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O at 256 and 384
 constexpr int kValueStages = 2;
 constexpr int kBadSlots = 4;       // marks of non-finite values: producers run at most three jobs ahead
 
-// A place in the work list: a job of a unit, and a tile of the job.  (Counts of one CTA and one unit fit 32 bits.)
+// A place in the work list: a job of a unit, and a tile of the job; `lead` is what is left there of the job's
+// start-up cost (see kJobCost).  (Counts of one CTA and one unit fit 32 bits.)
 struct Piece {
-  int32_t unit, job, tile;
+  int32_t unit, job, tile, lead;
 };
 
 struct __align__(16) Shared {
@@ -97,15 +102,17 @@ __host__ __device__ inline int64_t f16_tiles_before(int64_t n_w, int log2_job_to
 }
 
 __device__ __noinline__ Piece find_piece(const ChunkParams& p, int64_t g) {
-  const int64_t unit = g / p.tiles_per_unit, r = g - unit * p.tiles_per_unit;
+  const int64_t unit = g / p.unit_cost, r = g - unit * p.unit_cost;
+  const int64_t per_job = p.page_tiles + kJobCost;
   int64_t lo = 0, hi = p.jobs_per_unit - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
-    if (mid * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, mid) <= r) lo = mid;
+    if (mid * per_job + f16_tiles_before(p.n_w, p.log2_job_tokens, mid) <= r) lo = mid;
     else hi = mid - 1;
   }
-  const int64_t before = lo * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, lo);
-  return Piece{(int32_t)unit, (int32_t)lo, (int32_t)(r - before)};
+  const int64_t in_job = r - (lo * per_job + f16_tiles_before(p.n_w, p.log2_job_tokens, lo));
+  return Piece{(int32_t)unit, (int32_t)lo, (int32_t)(in_job > kJobCost ? in_job - kJobCost : 0),
+               (int32_t)(in_job < kJobCost ? kJobCost - in_job : 0)};
 }
 
 // A job's first chunk token, its tokens and its tiles.
@@ -692,17 +699,17 @@ static_assert(kKeyBytes<true> % 1024 == 0 && kKeySets<true> == kKeyStages, "a se
 // A CTA's walk over its pieces of the work list: `count` tiles from tile t_begin of one job of one unit.
 struct Walk {
   int32_t unit, job, t_begin, count;
-  int32_t left;          // tiles of the CTA from this piece on
+  int32_t left;          // cost left to the CTA from this piece on, without what is left of the job's start-up cost
   int32_t tokens, rows;  // chunk tokens and query rows of the job
   bool dual;             // streams: even and odd tiles of up to 128 rows (else two halves of the rows)
-  __device__ __forceinline__ Walk(const ChunkParams& p, const Piece& first, int32_t tiles)
-      : unit(first.unit), job(first.job), t_begin(first.tile), left(tiles) {
+  __device__ __forceinline__ Walk(const ChunkParams& p, const Piece& first, int32_t cost)
+      : unit(first.unit), job(first.job), t_begin(first.tile), left(cost - first.lead) {
     at(p);
   }
   __device__ __forceinline__ void at(const ChunkParams& p) {
     tokens = job_tokens(p, job);
     const int whole = job_tiles(p, job) - t_begin;
-    count = whole < left ? whole : left;
+    count = whole < left ? whole : left;  // <= 0: the end of the CTA's part
     rows = tokens << p.log2hg;
     dual = rows <= kRows;
   }
@@ -710,7 +717,7 @@ struct Walk {
   // Whether the piece is all of its job.
   __device__ __forceinline__ bool whole(const ChunkParams& p) const { return t_begin == 0 && count == job_tiles(p, job); }
   __device__ __forceinline__ void next(const ChunkParams& p) {
-    left -= count;
+    left -= count + kJobCost;
     t_begin = 0;
     if (++job == p.jobs_per_unit) {
       job = 0;
@@ -777,14 +784,14 @@ __device__ __forceinline__ void issue_pv_rows(uint32_t d, uint32_t pcol, uint64_
 // products is their idle time.  The softmax streams watch the operand tiles for it (see operands_ready).
 template <bool ROPE>
 __device__ __forceinline__ bool issue_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sk, uint32_t sv,
-                                           uint32_t tmem_, int32_t tiles_of_cta) {
+                                           uint32_t tmem_, int32_t cost_of_cta) {
   constexpr int KS = kKeyStages;
   const bool leader = tc::elect();
   const uint32_t tmem = uniform(tmem_);
   const uint64_t dq = tc::descriptor(sq), dk = tc::descriptor(sk), dv = tc::descriptor(sv), dv_rows = tc::descriptor_mn(sv);
   const uint64_t dq_lo = tc::descriptor16(sv + kValueStages * tc::kTileBytes), dk_lo = tc::descriptor16(sk + tc::kTileBytes);
   uint32_t kt = 0, vt = 0, jobs = 0, used0 = 0, used1 = 0;  // key and value tiles, pieces, steps of the streams so far
-  for (Walk w(p, sh.first, tiles_of_cta); uniform(w.left) > 0; w.next(p)) {
+  for (Walk w(p, sh.first, cost_of_cta); (int)uniform(w.count) > 0; w.next(p)) {
     const bool dual = uniform(w.dual);
     const int tiles = (int)uniform(w.count), steps = dual ? tiles : 2 * tiles;
     if (!wait(p, &sh.q_full[0], jobs & 1) || !wait(p, &sh.q_full[1], jobs & 1)) return false;
@@ -837,7 +844,7 @@ __device__ __forceinline__ int pages_of_warp(const ChunkParams& p, int64_t t_beg
 
 // Key producers: warp 0..3 of a set.
 template <int BK, bool ROPE, bool LUT>
-__device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int32_t tiles_of_cta,
+__device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint32_t sk, int32_t cost_of_cta,
                                          int set, int warp, int lane) {
   constexpr bool FRAG = BK != 0;
   constexpr int KS = kKeyStages, SETS = kKeySets<ROPE>;
@@ -845,7 +852,7 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
   uint32_t kt0 = 0, syncs = 0;
   // the warp's 32-token block: its page of a tile and its place in the page
   const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32;
-  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; w.next(p)) {
+  for (Walk w(p, sh.first, cost_of_cta); w.count > 0; w.next(p)) {
     const uint8_t* unit_pages = p.pages + w.unit * p.unit_page_stride;
     const uint16_t* rows = p.wk + w.unit * p.win_unit_stride;
     const uint16_t* fresh = p.k_new + w.unit * p.n * kD;
@@ -944,12 +951,12 @@ __device__ __forceinline__ bool key_role(const ChunkParams& p, Shared& sh, uint3
 
 // Value producers: warp 0..3.
 template <int BV, bool ROPE, bool LUT>
-__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int32_t tiles_of_cta,
+__device__ __forceinline__ bool value_role(const ChunkParams& p, Shared& sh, uint32_t sv, int32_t cost_of_cta,
                                            int warp, int lane) {
   constexpr bool FRAG = BV != 0;
   uint32_t kt = 0, jobs = 0, syncs = 0;
   const int in_tile = 32 * warp / p.R, block = (32 * warp - in_tile * p.R) / 32, half = p.G == 64 ? 1 : 0;
-  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; ++jobs, w.next(p)) {
+  for (Walk w(p, sh.first, cost_of_cta); w.count > 0; ++jobs, w.next(p)) {
     const uint8_t* unit_pages = p.pages + w.unit * p.unit_page_stride;
     const uint16_t* rows = p.wv + w.unit * p.win_unit_stride;
     const uint16_t* fresh = p.v_new + w.unit * p.n * kD;
@@ -1029,13 +1036,13 @@ __device__ __forceinline__ bool operands_ready(const ChunkParams& p, Shared& sh,
 
 template <bool FRAG, bool ROPE>
 __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, uint32_t sq, uint32_t sq_lo,
-                                             uint8_t* exchange, uint32_t tmem, int32_t tiles_of_cta, int q, int warp, int lane) {
+                                             uint8_t* exchange, uint32_t tmem, int32_t cost_of_cta, int q, int warp, int lane) {
   constexpr int KS = kKeyStages;
   const int r = 32 * warp + lane;
   const uint32_t my_s = tmem + 128 * q + ((uint32_t)(32 * warp) << 16), my_o = my_s + 256;
   const int hg = 1 << p.log2hg;
   uint32_t tiles0 = 0, done = 0, jobs = 0, finals = 0, halves = 0;  // tiles, steps, pieces, pieces with steps of this stream, exchanges so far
-  for (Walk w(p, sh.first, tiles_of_cta); w.left > 0; ++jobs, w.next(p)) {
+  for (Walk w(p, sh.first, cost_of_cta); w.count > 0; ++jobs, w.next(p)) {
     const int tiles = w.count;
     const int b = w.unit / p.Hkv, kvh = w.unit - b * p.Hkv;
     const int64_t head_row = (int64_t)b * p.Hq + kvh * hg, tok0 = w.tok0(p);  // query row (token i, head h): (head_row + h) * n + tok0 + i
@@ -1043,22 +1050,42 @@ __device__ __forceinline__ bool softmax_role(const ChunkParams& p, Shared& sh, u
     // product of the piece before has finished, and with it every earlier one that read the tile.
     {
       const int first = w.dual ? 64 * q : 128 * q, count = w.dual ? 64 : 128;
-      for (int task = warp; task < count / 8; task += 4) {
-        const int row = first + 8 * task + (lane & 7), c = lane >> 3;
-        uint4 v[4] = {};
-        if (row < w.rows) {
-          const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + tok0 + (row >> p.log2hg);
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + src_row * kD) + 4 * c;
+      // two eights of rows in flight per warp
+#pragma unroll 1
+      for (int task = warp; task < count / 8; task += 8) {
+        uint4 v[2][4] = {};
+        const int c = lane >> 3;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
+        for (int h = 0; h < 2; ++h) {
+          const int row = first + 8 * (task + 4 * h) + (lane & 7);
+          if (row < w.rows) {
+            const int64_t src_row = (head_row + (row & (hg - 1))) * p.n + tok0 + (row >> p.log2hg);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + src_row * kD) + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = __ldg(src + i);
+          }
         }
-        const uint32_t tile = sq + (row >> 7) * tc::kTileBytes;
-        if (FRAG && p.page_tiles > 0) {
-          store_frag_row(tile, row & 127, c, v);
-        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sts16(tile + tc::chunk_offset(c >> 1, row & 127, 4 * (c & 1) + i), v[i].x, v[i].y, v[i].z, v[i].w);
+        for (int h = 0; h < 2; ++h) {
+          const int row = first + 8 * (task + 4 * h) + (lane & 7);
+          const uint32_t tile = sq + (row >> 7) * tc::kTileBytes;
+          if (FRAG && p.page_tiles > 0) {
+            store_frag_row(tile, row & 127, c, v[h]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts16(tile + tc::chunk_offset(c >> 1, row & 127, 4 * (c & 1) + i), v[h][i].x, v[h][i].y, v[h][i].z, v[h][i].w);
+          }
+        }
+      }
+      // the next job's rows are on their way to L2 meanwhile
+      if (w.job + 1 < p.jobs_per_unit) {
+        const int row = (w.dual ? r : 128 * q + r);
+        const int64_t i = tok0 + w.tokens + (row >> p.log2hg);
+        if (i < p.n) {
+          const uint16_t* next = p.q + ((head_row + (row & (hg - 1))) * p.n + i) * kD;
+          prefetch_l2(next);
+          prefetch_l2(next + 64);
         }
       }
     }
@@ -1286,7 +1313,7 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   constexpr int kIssuer = kThreads<ROPE> / 32 - 1;
   const int64_t g_begin = (int64_t)blockIdx.x * p.per_cta;
-  const int32_t tiles_of_cta = (int32_t)min(p.per_cta, p.total_tiles - g_begin);
+  const int32_t cost_of_cta = (int32_t)min(p.per_cta, p.total_cost - g_begin);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -1323,22 +1350,22 @@ __global__ void __launch_bounds__(kThreads<ROPE>, 1) chunk_kernel(const __grid_c
 
   bool ok = true;
   if (warp < 8) {
-    ok = softmax_role<BK != 0, ROPE>(p, sh, sq, sv + kValueStages * tc::kTileBytes, base + tc::kTileBytes, tmem, tiles_of_cta, warp >> 2, warp & 3, lane);
+    ok = softmax_role<BK != 0, ROPE>(p, sh, sq, sv + kValueStages * tc::kTileBytes, base + tc::kTileBytes, tmem, cost_of_cta, warp >> 2, warp & 3, lane);
   } else if (warp < kIssuer) {
     const int i = warp - 8;
     if constexpr (BK != 0) {
       // expanding fragment-order pages, keys on warp schedulers 0 and 1 and values on 2 and 3: fewer different
       // loops per instruction cache
       const int block = (i >> 2) * 2 + (i & 1);
-      if (i & 2) ok = value_role<BV, ROPE, LUT>(p, sh, sv, tiles_of_cta, block, lane);
-      else ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, 0, block, lane);
+      if (i & 2) ok = value_role<BV, ROPE, LUT>(p, sh, sv, cost_of_cta, block, lane);
+      else ok = key_role<BK, ROPE, LUT>(p, sh, sk, cost_of_cta, 0, block, lane);
     } else if (i < kProducers) {
-      ok = value_role<BV, ROPE, LUT>(p, sh, sv, tiles_of_cta, i, lane);
+      ok = value_role<BV, ROPE, LUT>(p, sh, sv, cost_of_cta, i, lane);
     } else {
-      ok = key_role<BK, ROPE, LUT>(p, sh, sk, tiles_of_cta, i / kProducers - 1, i % kProducers, lane);
+      ok = key_role<BK, ROPE, LUT>(p, sh, sk, cost_of_cta, i / kProducers - 1, i % kProducers, lane);
     }
   } else {
-    ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, tiles_of_cta);
+    ok = issue_role<ROPE>(p, sh, sq, sk, sv, tmem, cost_of_cta);
   }
   if (!ok) report_error(p.err, kDevWaitTimeout);
   __syncwarp();
@@ -1411,7 +1438,7 @@ cudaError_t launch_t(const ChunkParams& p, int64_t grid, int* launches, cudaStre
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (grid == 1 || p.per_cta % p.tiles_per_unit == 0) return cudaSuccess;  // no cut inside a job
+  if (grid == 1 || p.per_cta % p.unit_cost == 0) return cudaSuccess;  // no cut inside a job
   cudaLaunchConfig_t cfg{};
   const int64_t by = (p.rows_max + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
   cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)by);
@@ -1444,10 +1471,11 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   p.jobs_per_unit = (p.n + job_tokens - 1) / job_tokens;
   p.tiles_per_unit = p.jobs_per_unit * p.page_tiles + f16_tiles_before(p.n_w, p.log2_job_tokens, p.jobs_per_unit - 1) +
                      ((p.n_w + p.n + 127) >> 7);
-  p.total_tiles = p.n_units * p.tiles_per_unit;
-  int64_t grid = p.total_tiles < sm_count ? p.total_tiles : sm_count;
-  p.per_cta = (p.total_tiles + grid - 1) / grid;
-  grid = (p.total_tiles + p.per_cta - 1) / p.per_cta;
+  p.unit_cost = p.tiles_per_unit + kJobCost * p.jobs_per_unit;
+  p.total_cost = p.n_units * p.unit_cost;
+  int64_t grid = p.total_cost < sm_count ? p.total_cost : sm_count;
+  p.per_cta = (p.total_cost + grid - 1) / grid;
+  grid = (p.total_cost + p.per_cta - 1) / p.per_cta;
   if (p.per_cta >= ((int64_t)1 << 31) || p.jobs_per_unit >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
   p.rows_max = (int32_t)slot_rows(p.n, hg);
   p.part_first = workspace;

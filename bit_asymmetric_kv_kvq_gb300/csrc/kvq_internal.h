@@ -193,7 +193,7 @@ struct ChunkParams {
   int32_t test_withhold;
   int32_t pages_per_tile;   // the rest is set by the launcher
   int64_t page_tiles;       // page tiles of a unit
-  int64_t jobs_per_unit, tiles_per_unit, total_tiles, per_cta;
+  int64_t jobs_per_unit, tiles_per_unit, unit_cost, total_cost, per_cta;  // costs in tiles
   int32_t log2_job_tokens;  // tokens of a job
   int32_t rows_max;         // rows a partial slot holds
   void* part_first;         // [grid] where every CTA's part of the list begins
