@@ -476,6 +476,7 @@ kvq_status launch_chunk_for(kvq_cache* c, const void* k, const void* v, const vo
   int launches = 0;
   const cudaError_t e = kvq::launch_chunk(p, c->cfg.rope != 0, c->sm_count, workspace, &launches, s);
   c->launches += launches;
+  if (e == cudaErrorNotSupported && launches == 0) return KVQ_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KVQ_OK : fail_cuda(c);
 }
 

@@ -8,14 +8,15 @@
 // Work list.  A job is up to 256 query rows of one (sequence, kv head) unit -- the chunk's tokens with the
 // heads that share the kv head beside each other, so grouped heads fill the tiles -- and a tile is up
 // to 128 keys: whole pages first, then the unit's fp16 rows (sink, window) followed by the new tokens as
-// far as the job's last token sees.  The flat list of all jobs' tiles is cut into equal contiguous
-// pieces, one per SM, so few rows over a long cache are spread over the whole GPU and many rows leave no
-// partly filled last wave.  A job that a cut divides leaves unnormalised partials (m, l, acc) in the
+// far as the job's last token sees.  The flat list of all jobs' tiles (and start-ups, kJobCost) is cut into
+// contiguous pieces of equal cost, one per SM, so few rows over a long cache are spread over the whole GPU
+// and many rows leave no partly filled last wave.  A job that a cut divides leaves unnormalised partials (m, l, acc) in the
 // workspace, at most two per CTA, and merge_chunk_kernel joins them in CTA order.
 //
-// A CTA.  Eight producer warps expand codes into fp16 operand tiles in shared memory (four for keys, four
-// for values), one thread issues the products, and two groups of four warps, a thread per query row, turn
-// S = Q K^T into P (fp16, back into tensor memory over S).  The two groups are two streams whose products
+// A CTA.  Producer warps expand codes into fp16 operand tiles in shared memory (four for keys -- two sets of
+// four, taking turns, where keys are rotated -- and four for values; new tokens are copied as they are), one
+// thread issues the products, and two groups of four warps, a thread per query row, turn S = Q K^T into P
+// (fp16, back into tensor memory over S).  The two groups are two streams whose products
 // alternate, PV of one after QK of the other, so the tensor cores work on one stream while the other is in
 // its softmax.  With more than 128 rows the streams are the two halves of the rows over the same key
 // tiles; with up to 128 they are the even and the odd key tiles of the same rows, joined at the end
@@ -26,9 +27,30 @@
 // 1e-3 of a weight.  A constant added to a channel of ALL keys shifts every score of a row alike and
 // cancels in the softmax, so keys enter as k - mu_c with mu_c the centre of the channel's range in one page
 // where that centre lies outside the range's own width (else 0): the large common part is gone before
-// rounding.  Rotated keys have no such constant: they enter as hi + lo, two fp16 halves and two
-// products (22 bits).  Weights are rounded to fp16 scaled by 2^7, so a weight down to 2^-31 of the
-// maximum still counts; values z + s c are rounded once.
+// rounding.  Rotated keys have no such constant: they are rounded to fp16, and what that leaves over of the
+// eight pairs of channels that hold the outliers enters through a 16-column product of its own (22 bits there;
+// a low half of all channels made the product and the tile half as expensive again).  Weights are rounded to
+// fp16 scaled by 2^7, so a weight down to 2^-31 of the maximum still counts; values z + s c are rounded once.
+//
+// What bounds it (GB300; 1863 TFLOP/s bf16 and 6801 GB/s measured, 4 D flops per visible pair of query and key):
+//   A  512 tokens, batch 4 x 40 heads over 8192 tokens, K4V2      372 us   354 GFLOP: 950 TFLOP/s, 0.51
+//   B  a whole prompt of 4099 tokens, batch 2 x 32 heads on 8     343 us   275 GFLOP: 803 TFLOP/s, 0.43 (kvq_chunk_step)
+//   C  8 tokens, batch 32 x 32 heads on 8 over 32768, K2V2        566 us   824 MB of pages: 1.46 TB/s, 0.21
+//   D  33 tokens, 32 heads on 8 over 1,048,576, K3V3, rotated     2.24 ms  567 GFLOP of 146 us of pages
+// Long chunks (A, B): the softmax.  Every score passes tensor memory twice, through one exponential and several
+// conversions, while the product of its tile takes a quarter of that time; the two streams hide the products under
+// it.  Few rows (C, D): the producers.  Every code becomes 16 bits of an operand tile once per job, 32,768 elements a
+// tile (2,700 cycles in C; 10,700 in D, where each pair of channels of a key takes a sine and a cosine besides), and
+// the products' 128 rows cost the same whether they are used or not.
+//
+// Steps that paid, in us of the workloads in that order (A, B, C, D): roles for warps instead of one block that does
+// everything in turn, A 980 -> 461, B 1255 -> 660, C 1366 -> 723; an issuing warp that waits once a step, A 461 -> 391,
+// C 723 -> 616; a row of codes in registers, a low tile of 16 columns and two producer sets for rotated keys,
+// D 4531 -> 2365; S read once, A 399 -> 384; zero points prepared once per block, C 655 -> 576; new tokens copied
+// straight into place, B 528 -> 451; start-up costs in the cuts, B 451 -> 343.  Tried and slower: unrolled producer
+// loops (instruction-cache misses), a 16-column double-buffered softmax, 64 columns a pass with registers moved
+// between warpgroups (spills), sixteen softmax warps, both streams on both halves of the rows, two sets of key
+// producers where keys are not rotated.
 #include <atomic>
 #include <cstddef>
 
@@ -403,6 +425,65 @@ __device__ __forceinline__ float code_float(uint32_t codes, int shift, uint32_t 
   return __uint_as_float(((codes >> shift) & mask) | 0x4B000000u) - 8388608.0f;
 }
 
+// Sparse entries of a lane's token of a bitstream page, over the dense key the lane has written: an entry's channel and
+// its rotation partner are made again and stored.  (Within the loop over the octets an entry costs all lanes a select
+// over eight channels in every octet that any lane has one in.)
+template <bool ROPE, bool LUT>
+__device__ __forceinline__ void sparse_pairs(const ChunkParams& p, const Shared& sh, const uint8_t* page, int tk, int row,
+                                             const uint32_t* meta, uint32_t pos, const uint8_t* lo_slot, uint32_t tile) {
+  uint32_t sp[4];  // channel << 16 | fp16 bits
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    sp[e] = 0xFFFFFFFFu;
+    if (e < p.nsp)
+      sp[e] = (uint32_t)page[p.lay.off_si + tk * p.nsp + e] << 16 |
+              reinterpret_cast<const uint16_t*>(page + p.lay.off_sv)[tk * p.nsp + e];
+  }
+  const int bits = p.bk;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(page + p.lay.off_kc) + tk * 4 * bits;
+#pragma unroll 1
+  for (int e = 0; e < p.nsp; ++e) {
+    const uint32_t s = sp[0];
+    const int c = (int)(s >> 16) & 127, partner = c ^ 64, pair = c & 63;
+    const int at = partner * bits, word = at >> 5;
+    const uint32_t code = __funnelshift_r(__ldg(codes + word), __ldg(codes + min(word + 1, 4 * bits - 1)), at & 31);
+    const float2 zs = __half22float2(h2(meta[partner]));
+    const uint32_t mask = (1u << bits) - 1u;
+    float u = fmaf(zs.y, LUT ? sh.k_lev[code & mask] : code_float(code, 0, mask), zs.x);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)  // unless the partner is an entry too
+      if ((int)(sp[i] >> 16) == partner) u = __half2float(__ushort_as_half((uint16_t)sp[i]));
+    const float v = __half2float(__ushort_as_half((uint16_t)s));
+    float x = c < 64 ? v : u, y = c < 64 ? u : v;
+    if constexpr (ROPE) {
+      const unsigned long long t = sh.turns[pair];
+      const float2 cs = key_turn(pos, make_uint2((uint32_t)t, (uint32_t)(t >> 32)));
+      const float a = x * cs.x - y * cs.y, b = x * cs.y + y * cs.x;
+      x = a;
+      y = b;
+    } else {
+      x -= __half2float(reinterpret_cast<const __half*>(sh.mu)[pair]);
+      y -= __half2float(reinterpret_cast<const __half*>(sh.mu)[64 + pair]);
+    }
+    const __half hx = __float2half_rn(x), hy = __float2half_rn(y);
+    sts2(tile + tc::chunk_offset(0, row, pair >> 3) + 2 * (pair & 7), __half_as_ushort(hx));
+    sts2(tile + tc::chunk_offset(1, row, pair >> 3) + 2 * (pair & 7), __half_as_ushort(hy));
+    if constexpr (ROPE) {
+      const uint32_t j = lo_slot[pair];
+      if (j != 255u) {
+        const uint32_t lo = tile + tc::kTileBytes;
+        sts2(lo + tc::offset16(row, j), __half_as_ushort(__float2half_rn(x - __half2float(hx))));
+        sts2(lo + tc::offset16(row, 8 + j), __half_as_ushort(__float2half_rn(y - __half2float(hy))));
+      }
+    }
+    // the next entry to the front; the others stay in sight
+    sp[0] = sp[1];
+    sp[1] = sp[2];
+    sp[2] = sp[3];
+    sp[3] = s;
+  }
+}
+
 // Keys of a 32-token block of a bitstream page, for one warp: lane = token, its row of codes in registers, an
 // octet of channels and their rotation partners at a time.  meta: the group's 128 zero point / step words in
 // shared memory.
@@ -422,14 +503,6 @@ __device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Share
         w[h][2 * i] = v.x;
         w[h][2 * i + 1] = v.y;
       }
-  uint32_t sp[4];  // sparse entries: channel << 16 | fp16 bits
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    sp[e] = 0xFFFFFFFFu;
-    if (e < p.nsp)
-      sp[e] = (uint32_t)page[p.lay.off_si + tk * p.nsp + e] << 16 |
-              reinterpret_cast<const uint16_t*>(page + p.lay.off_sv)[tk * p.nsp + e];
-  }
 #pragma unroll 1
   for (int q = 0; q < 8; ++q) {
     float x[8], y[8];
@@ -449,22 +522,9 @@ __device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Share
       for (int i = 0; i < 7; ++i) w[h][i] = __funnelshift_rc(w[h][i], w[h][i + 1], 8 * bits);
       w[h][7] = __funnelshift_rc(w[h][7], 0u, 8 * bits);
     }
-#pragma unroll 1
-    for (int e = 0; e < p.nsp; ++e) {
-      const uint32_t s = e == 0 ? sp[0] : e == 1 ? sp[1] : e == 2 ? sp[2] : sp[3];
-      if (((s >> 19) & 7u) != (uint32_t)q) continue;  // of this octet or its partner
-      const float v = __half2float(__ushort_as_half((uint16_t)s));
-      const int k0 = (s >> 16) & 7;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k == k0) {
-          if (s >> 22) y[k] = v;
-          else x[k] = v;
-        }
-      }
-    }
     store_key_octets<ROPE>(p, sh, tile, row, q, pos, lo_slot, x, y);
   }
+  if (p.nsp) sparse_pairs<ROPE, LUT>(p, sh, page, tk, row, reinterpret_cast<const uint32_t*>(meta), pos, lo_slot, tile);
 }
 
 // Codes of channels 8 oct .. 8 oct + 7 of a bitstream row (4 * bits words).
@@ -1396,9 +1456,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunk_kernel(const __grid
       const int64_t slot = 2 * c + (c == c0 ? 1 : 0);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.rows_max + r) * 2);
       const float4 v = *reinterpret_cast<const float4*>(p.part_acc + (slot * p.rows_max + r) * kD + 4 * lane);
-      const float m = fmaxf(M, ml.x);
-      const float fo = M == -INFINITY ? 0.0f : exp2f(M - m), fn = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - m);
       if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // no key of that piece is visible to the row
+      const float m = fmaxf(M, ml.x);
+      const float fo = M == -INFINITY ? 0.0f : exp2f(M - m), fn = ml.x == -INFINITY ? 1.0f : exp2f(ml.x - m);
       L = L * fo + ml.y * fn;
       a.x = a.x * fo + v.x * fn;
       a.y = a.y * fo + v.y * fn;
@@ -1476,7 +1536,7 @@ cudaError_t launch_chunk(ChunkParams p, bool rope, int sm_count, void* workspace
   int64_t grid = p.total_cost < sm_count ? p.total_cost : sm_count;
   p.per_cta = (p.total_cost + grid - 1) / grid;
   grid = (p.total_cost + p.per_cta - 1) / p.per_cta;
-  if (p.per_cta >= ((int64_t)1 << 31) || p.jobs_per_unit >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
+  if (p.per_cta >= ((int64_t)1 << 31)) return cudaErrorNotSupported;  // days of work: refused before any
   p.rows_max = (int32_t)slot_rows(p.n, hg);
   p.part_first = workspace;
   p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + sm_count * kFirstBytes);

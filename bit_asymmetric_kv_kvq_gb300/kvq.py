@@ -467,6 +467,8 @@ def rope(cfg: kvq_rope_config, tensors, positions=0, rotate=None, outs=None, out
         pos = positions
     else:
         pos0 = int(positions)
+        if not -2**63 <= pos0 < 2**63:
+            raise ValueError("positions: need 64-bit numbers")
     index = dev.index
     args = (cfg, parts, types[dtype], types[odtype], B, n, pos, pos0, _stream(stream, index))
     if torch.cuda.current_device() == index:
@@ -585,6 +587,8 @@ class KVCache:
                     workspace = self.chunk_workspace(n)
         else:
             self._need(out, (B, Hq, n, D), "out")
+        if any(t.device.index != self.device for t in (k, v, q, out)):
+            raise ValueError(f"need tensors on cuda:{self.device}")
         if not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
             raise ValueError("workspace: need a contiguous CUDA tensor on the cache's device")
         status = getattr(lib(), call)(self.handle, k.data_ptr(), v.data_ptr(), q.data_ptr(), n, out.data_ptr(),

@@ -205,17 +205,19 @@ kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_f16, const void* v_f
  * q arrives rotated.  n_tokens >= 1, T + n_tokens < 2^31; whether the tokens fit the cache is not checked here.
  *
  * Keys and values are expanded to fp16 for the tensor cores (keys as differences from a per-channel
- * offset that cancels in the softmax, or as a high and a low half when they are rotated), products
- * accumulate in fp32, the softmax statistics are fp32, and the weights are rounded to fp16 before
- * the value product.  Outputs stay within a max relative error of 2e-3 per row of exact attention over the
- * dequantized cache and the chunk, like kvq_decode_attention's.  fp16's range is the limit: keys are finite for
- * |k| <= 61,408 (46,000 when they are rotated).  Sums are taken in a fixed order: outputs are bitwise
+ * offset that cancels in the softmax; rotated keys as they are, with a second fp16 part for the eight pairs of channels
+ * that hold the unit's outliers), products accumulate in fp32, the softmax statistics are fp32, and the weights are
+ * rounded to fp16 before the value product.  Outputs stay within a max relative error of 2e-3 per row of exact
+ * attention over the dequantized cache and the chunk, like kvq_decode_attention's, as long as the keys' rounding allows
+ * it: what is rounded once (the differences; rotated keys outside those pairs) has rms(q) * rms(k) <= 4 per channel at
+ * softmax_scale = D^-1/2.  fp16's range is the limit: keys are finite for |k| <= 61,408 (46,000 when they are rotated).  Sums are taken in a fixed order: outputs are bitwise
  * reproducible.  A token that a query does not attend cannot change its output, whatever it holds.
  *
  * workspace: device memory of at least kvq_chunk_workspace bytes, 16-byte aligned; it holds partial
  * results of one call, so calls that may overlap on the GPU (other streams, graphs replayed at the
  * same time) need one each, while calls in order on one stream -- all layers of a model -- share it.
- * KVQ_ERR_INVALID_ARG when it is null or too small.
+ * KVQ_ERR_INVALID_ARG when it is null or too small; KVQ_ERR_UNSUPPORTED when one SM's share of the call would exceed
+ * 2^31 tiles of 256 queries x 128 keys.
  */
 kvq_status kvq_chunk_attention(kvq_cache* cache, const void* k_f16, const void* v_f16, const void* q_f16,
                                int64_t n_tokens, void* out_f16, void* workspace, int64_t workspace_bytes,
@@ -519,7 +521,7 @@ typedef struct {
 
 typedef struct {
   const void* x;            /* device, x_type: element (b, t, h, c) at x + b*x_batch_stride + t*x_token_stride + h*x_head_stride + c */
-  void* out;                /* device, out_type, likewise; may be x itself (same type and strides), must not overlap otherwise */
+  void* out;                /* device, out_type, likewise; may be x itself (same type and strides, else KVQ_ERR_INVALID_ARG), must not overlap otherwise */
   int64_t x_batch_stride, x_token_stride, x_head_stride;       /* elements */
   int64_t out_batch_stride, out_token_stride, out_head_stride; /* elements */
   int32_t num_heads;

@@ -53,6 +53,13 @@ def test_rope_checks_arguments_on_the_host(kvq, kw, expect):
     assert _rope(kvq, **kw) == expect
 
 
+@pytest.mark.parametrize("kw", [dict(x_type=1), dict(out_type=2), dict(batch=2, part=dict(out_batch_stride=256)),
+                                dict(n=2, part=dict(out_token_stride=256)),
+                                dict(part=dict(num_heads=2, out_head_stride=256))])
+def test_rope_in_place_needs_the_same_layout(kvq, kw):
+    assert _rope(kvq, **kw) == -1
+
+
 def test_rope_nulls(kvq):
     L = kvq.lib()
     cfg = kvq.make_rope_config(128)
