@@ -487,22 +487,21 @@ __device__ __forceinline__ void sparse_pairs(const ChunkParams& p, const Shared&
 // Keys of a 32-token block of a bitstream page, for one warp: lane = token, its row of codes in registers, an
 // octet of channels and their rotation partners at a time.  meta: the group's 128 zero point / step words in
 // shared memory.
-template <bool ROPE, bool LUT>
-__device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
+template <int BITS, bool ROPE, bool LUT>
+__device__ __forceinline__ void key_block_dense(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
                                                int slot, const uint4* meta, uint32_t pos, const uint8_t* lo_slot,
                                                uint32_t tile, int lane) {
-  const int bits = p.bk, tk = 32 * block + lane, row = 32 * slot + lane;
-  const uint32_t mask = (1u << bits) - 1u;
-  uint32_t w[2][8] = {};  // codes of channels 0..63 and 64..127: 2 * bits words each
+  const int tk = 32 * block + lane, row = 32 * slot + lane;
+  constexpr uint32_t mask = (1u << BITS) - 1u;
+  uint32_t w[2][2 * BITS];  // codes of channels 0..63 and 64..127
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < bits) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(page + p.lay.off_kc) + (tk * 2 + h) * bits + i);
-        w[h][2 * i] = v.x;
-        w[h][2 * i + 1] = v.y;
-      }
+    for (int i = 0; i < BITS; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(page + p.lay.off_kc) + (tk * 2 + h) * BITS + i);
+      w[h][2 * i] = v.x;
+      w[h][2 * i + 1] = v.y;
+    }
 #pragma unroll 1
   for (int q = 0; q < 8; ++q) {
     float x[8], y[8];
@@ -514,17 +513,27 @@ __device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Share
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float2 zs = __half22float2(h2(m[k]));
-        const float c = LUT ? sh.k_lev[(w[h][0] >> (bits * k)) & mask] : code_float(w[h][0], bits * k, mask);
+        const float c = LUT ? sh.k_lev[(w[h][0] >> (BITS * k)) & mask] : code_float(w[h][0], BITS * k, mask);
         o[k] = fmaf(zs.y, c, zs.x);
       }
       // the next octet's codes to the front
 #pragma unroll
-      for (int i = 0; i < 7; ++i) w[h][i] = __funnelshift_rc(w[h][i], w[h][i + 1], 8 * bits);
-      w[h][7] = __funnelshift_rc(w[h][7], 0u, 8 * bits);
+      for (int i = 0; i < 2 * BITS; ++i) w[h][i] = __funnelshift_rc(w[h][i], i + 1 < 2 * BITS ? w[h][i + 1] : 0u, 8 * BITS);
     }
     store_key_octets<ROPE>(p, sh, tile, row, q, pos, lo_slot, x, y);
   }
-  if (p.nsp) sparse_pairs<ROPE, LUT>(p, sh, page, tk, row, reinterpret_cast<const uint32_t*>(meta), pos, lo_slot, tile);
+}
+
+template <bool ROPE, bool LUT>
+__device__ __forceinline__ void key_block_bits(const ChunkParams& p, const Shared& sh, const uint8_t* page, int block,
+                                               int slot, const uint4* meta, uint32_t pos, const uint8_t* lo_slot,
+                                               uint32_t tile, int lane) {
+  if (p.bk == 2) key_block_dense<2, ROPE, LUT>(p, sh, page, block, slot, meta, pos, lo_slot, tile, lane);
+  else if (p.bk == 3) key_block_dense<3, ROPE, LUT>(p, sh, page, block, slot, meta, pos, lo_slot, tile, lane);
+  else key_block_dense<4, ROPE, LUT>(p, sh, page, block, slot, meta, pos, lo_slot, tile, lane);
+  if (p.nsp)
+    sparse_pairs<ROPE, LUT>(p, sh, page, 32 * block + lane, 32 * slot + lane, reinterpret_cast<const uint32_t*>(meta), pos,
+                            lo_slot, tile);
 }
 
 // Codes of channels 8 oct .. 8 oct + 7 of a bitstream row (4 * bits words).
