@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include "kvq.h"
+#include "kvq_chunk.h"
 #include "kvq_internal.h"
 
 namespace {

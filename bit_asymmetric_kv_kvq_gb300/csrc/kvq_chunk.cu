@@ -36,27 +36,29 @@
 //   A  512 tokens, batch 4 x 40 heads over 8192 tokens, K4V2      372 us   354 GFLOP: 950 TFLOP/s, 0.51
 //   B  a whole prompt of 4099 tokens, batch 2 x 32 heads on 8     343 us   275 GFLOP: 803 TFLOP/s, 0.43 (kvq_chunk_step)
 //   C  8 tokens, batch 32 x 32 heads on 8 over 32768, K2V2        566 us   824 MB of pages: 1.46 TB/s, 0.21
-//   D  33 tokens, 32 heads on 8 over 1,048,576, K3V3, rotated     2.24 ms  567 GFLOP of 146 us of pages
-// Long chunks (A, B): the softmax.  Every score passes tensor memory twice, through one exponential and several
-// conversions, while the product of its tile takes a quarter of that time; the two streams hide the products under
-// it.  Few rows (C, D): the producers.  Every code becomes 16 bits of an operand tile once per job, 32,768 elements a
-// tile (2,700 cycles in C; 10,700 in D, where each pair of channels of a key takes a sine and a cosine besides), and
-// the products' 128 rows cost the same whether they are used or not.
+//   D  33 tokens, 32 heads on 8 over 1,048,576, K3V3, rotated     2.08 ms  567 GFLOP, 990 MB of pages
+// Long chunks (A, B): a tile of 256 rows x 128 keys takes 4,050 cycles, its products 2,740 at the matrix rate; the
+// softmax of either stream (every score through tensor memory twice, an exponential, the rounding) is about as long as
+// both streams' products, which hide it only in part, and a job's start and end cost another 13,000 cycles.  Few rows
+// (C, D): the producers.  Every code becomes 16 bits of an operand tile once per job, 32,768 elements a tile (2,700
+// cycles in C; 10,000 in D, where each pair of channels of a key takes a sine and a cosine besides), and the products'
+// 128 rows cost the same whether they are used or not.
 //
-// Steps that paid, in us of the workloads in that order (A, B, C, D): roles for warps instead of one block that does
-// everything in turn, A 980 -> 461, B 1255 -> 660, C 1366 -> 723; an issuing warp that waits once a step, A 461 -> 391,
-// C 723 -> 616; a row of codes in registers, a low tile of 16 columns and two producer sets for rotated keys,
-// D 4531 -> 2365; S read once, A 399 -> 384; zero points prepared once per block, C 655 -> 576; new tokens copied
-// straight into place, B 528 -> 451; start-up costs in the cuts, B 451 -> 343.  Tried and slower: unrolled producer
-// loops (instruction-cache misses), a 16-column double-buffered softmax, 64 columns a pass with registers moved
-// between warpgroups (spills), sixteen softmax warps, both streams on both halves of the rows, two sets of key
-// producers where keys are not rotated.
+// Steps that paid, in us of the workloads above: roles for warps instead of one block that does everything in turn,
+// A 980 -> 461, B 1255 -> 660, C 1366 -> 723; an issuing warp that waits once a step, A 461 -> 391, C 723 -> 616; a row
+// of codes in registers, a low tile of 16 columns and two producer sets for rotated keys, D 4531 -> 2365; S read once,
+// A 399 -> 384; zero points prepared once per block, C 655 -> 576; new tokens copied straight into place, B 528 -> 451;
+// start-up costs in the cuts, B 451 -> 343; sparse entries written over the dense keys and loops compiled per code
+// width, D 2252 -> 2077.  Tried and slower: unrolled producer loops (instruction-cache misses), a 16-column
+// double-buffered softmax, 64 columns a pass with registers moved between warpgroups (spills), sixteen softmax warps,
+// both streams on both halves of the rows, two sets of key producers where keys are not rotated, bitstream zero points
+// and steps converted once per block (D 2108), value codes fetched an octet ahead (D 2080).
 #include <atomic>
 #include <cstddef>
 
 #include <cuda_fp16.h>
 
-#include "kvq_internal.h"
+#include "kvq_chunk.h"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
@@ -158,6 +160,13 @@ __device__ __forceinline__ void sts4(uint32_t addr, uint32_t a) {
 __device__ __forceinline__ void sts2(uint32_t addr, uint16_t a) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(a) : "memory");
 }
+// 16 bytes into shared memory asynchronously, or zeros (src is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src_gmem, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src_gmem), "r"(copy ? 16 : 0)
+               : "memory");
+}
+template <int N>  // all but the newest N groups
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 

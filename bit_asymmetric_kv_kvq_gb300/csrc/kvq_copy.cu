@@ -14,7 +14,7 @@
 // Measured (GB300): half of 32 sequences of 32768 tokens x 8 heads replaced in place, 819 MB read and
 // written, 129 us (6.35 TB/s); with the index looked up per sequence and thread instead of a list of the
 // sequences that move, 171 us.
-#include "kvq_internal.h"
+#include "kvq_chunk.h"
 #include "kvq_ptx.cuh"
 
 namespace kvq {
