@@ -13,7 +13,9 @@
 //
 // Measured (GB300): half of 32 sequences of 32768 tokens x 8 heads replaced in place, 819 MB read and
 // written, 129 us (6.35 TB/s); with the index looked up per sequence and thread instead of a list of the
-// sequences that move, 171 us.
+// sequences that move, 171 us.  One sequence of 4096 tokens x 32 heads into eight, 129 MB, 23.9 us (5.38 TB/s); with one
+// column's loads in flight at a time, 26.6 us; 32 sequences of 8192 tokens x 8 heads in another order, 715 MB, 113 us
+// (6.35 TB/s; 182 us).
 #include "kvq_chunk.h"
 #include "kvq_ptx.cuh"
 
@@ -119,34 +121,31 @@ __global__ void __launch_bounds__(128) reorder_sequences_kernel(const CopySequen
   }
 }
 
-// Into another cache: a few moves' loads together, then their stores; a source that follows itself is read once.
-// A thread takes kColumns columns, so the list of moves is made for four times as many bytes.
+// Into another cache.  A thread takes kColumns columns: their loads are in flight together, the list of moves is made for
+// more bytes, and a source that follows itself is read once.
 constexpr int kColumns = 4;
 
 __global__ void __launch_bounds__(256) copy_sequences_kernel(const CopySequencesParams p) {
   __shared__ int2 moves[kMoves];
   __shared__ int n_moves;
+  const int64_t col0 = (int64_t)blockIdx.x * kColumns * blockDim.x + threadIdx.x;
+  const Column c[kColumns] = {{p, col0}, {p, col0 + blockDim.x}, {p, col0 + 2 * blockDim.x}, {p, col0 + 3 * blockDim.x}};
+  uint4 v[kColumns] = {};
+  int held = -1;
   for (int b = 0; b < p.n_dst; b += kMoves) {
     const int n = list_moves(p, b, min(b + kMoves, p.n_dst), moves, &n_moves);
-#pragma unroll 1
-    for (int col = 0; col < kColumns; ++col) {
-      const Column c(p, ((int64_t)blockIdx.x * kColumns + col) * blockDim.x + threadIdx.x);
-      if (!c.live) break;
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        uint4 v[8];
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const int2 m = moves[i];
+      if (m.y != held) {
+        held = m.y;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (i0 + k >= n) break;
-          const int from = moves[i0 + k].y;
-          if (k > 0 && from == moves[i0 + k - 1].y) v[k] = v[k - 1];
-          else v[k] = __ldg(reinterpret_cast<const uint4*>(c.src + from * c.src_seq));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (i0 + k >= n) break;
-          *reinterpret_cast<uint4*>(c.dst + moves[i0 + k].x * c.dst_seq) = v[k];
-        }
+        for (int k = 0; k < kColumns; ++k)
+          if (c[k].live) v[k] = __ldg(reinterpret_cast<const uint4*>(c[k].src + m.y * c[k].src_seq));
       }
+#pragma unroll
+      for (int k = 0; k < kColumns; ++k)
+        if (c[k].live) *reinterpret_cast<uint4*>(c[k].dst + m.x * c[k].dst_seq) = v[k];
     }
   }
 }
