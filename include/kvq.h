@@ -208,9 +208,12 @@ kvq_status kvq_append_chunk(kvq_cache* cache, const void* k_f16, const void* v_f
  * offset that cancels in the softmax; rotated keys as they are, with a second fp16 part for the eight pairs of channels
  * that hold the unit's outliers), products accumulate in fp32, the softmax statistics are fp32, and the weights are
  * rounded to fp16 before the value product.  Outputs stay within a max relative error of 2e-3 per row of exact
- * attention over the dequantized cache and the chunk, like kvq_decode_attention's, as long as the keys' rounding allows
- * it: what is rounded once (the differences; rotated keys outside those pairs) has rms(q) * rms(k) <= 4 per channel at
- * softmax_scale = D^-1/2.  fp16's range is the limit: keys are finite for |k| <= 61,408 (46,000 when they are rotated).  Sums are taken in a fixed order: outputs are bitwise
+ * attention over the dequantized cache and the chunk, like kvq_decode_attention's, for keys whose outliers keep to their
+ * channels (with rope = 1 at most eight pairs of them).  In general e, the largest error of a row's scores, is at most
+ * softmax_scale * sum_c |q_c| 2^-11 |x_c|, x being what is rounded once (the differences; the channels outside those
+ * pairs), and the row's error grows by 2e times the spread of its values: sparse entries of 25 that change their
+ * channels from token to token measure 2.1e-3 on rotated 3-bit keys.  fp16's range is the limit: keys are finite for
+ * |k| <= 61,408 (46,000 when they are rotated).  Sums are taken in a fixed order: outputs are bitwise
  * reproducible.  A token that a query does not attend cannot change its output, whatever it holds.
  *
  * workspace: device memory of at least kvq_chunk_workspace bytes, 16-byte aligned; it holds partial

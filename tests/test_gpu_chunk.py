@@ -164,6 +164,55 @@ def test_chunk_attention_and_step(method, B, Hkv, hg, T, n, sink):
     cache.close()
 
 
+@pytest.mark.parametrize("method", ["k3v3", "k3v3rope", "k4v2rope", "lut33", "k2v2r32sp"])
+def test_sparse_entries_in_both_channels_of_a_pair(method):
+    """Entries c and c + 64 of one token are the two halves of a rotated pair, and their places change from token to
+    token, so the scores themselves are rounded coarsely.  The bound per row: a key's channel is rounded to fp16 once (half
+    a step: 2^-11 of it) after a rotation whose sine and cosine are off by 2^-20, so score j is off by at most e_j =
+    scale sum_c |q_c| (2^-11 |k_c| + 2^-19 |k_pair|); mu is 0 here (the ranges hold 0 well inside).  With e the largest,
+    weights p_j move by factors within exp(+-2e) that keep their sum, so the output by at most expm1(2e) sum_j p_j |v_j - o|;
+    weights and values are rounded once each (2^-11, 2^-11 of |v_j|) and so is the output."""
+    kvq = _kvq()
+    B, Hkv, hg, T, n = 1, 2, 4, 420, 6
+    w = _workload(method, B, Hkv, hg, T, n)
+    K, V, q = _inputs(w, T, n)
+    rng = np.random.default_rng(11)
+    K = np.clip(K, -1, 1)
+    for t in range(T):
+        c = int(rng.integers(0, 64)) if t % 3 else 5
+        K[:, :, t, c] = 25.0 * rng.choice([-1.0, 1.0], K[:, :, t, c].shape)
+        if t % 2:
+            K[:, :, t, c + 64] = 24.0 * rng.choice([-1.0, 1.0], K[:, :, t, c].shape)
+    K = np.ascontiguousarray(K.astype(np.float16))
+    cache = kvq.KVCache.for_workload(w, max_tokens=T + n)
+    cache.prefill_quantize(_dev(K[:, :, :T]), _dev(V[:, :, :T]))
+    units = {(b, h): _unit(w, K[b, h, :T], V[b, h, :T]) for b in range(B) for h in range(Hkv)}
+    out = cache.chunk_attention(_dev(K[:, :, T:]), _dev(V[:, :, T:]), _dev(q)).float().cpu().numpy().astype(np.float64)
+    assert cache.sync_status() == 0
+    worst = 0.0
+    for (b, h), u in units.items():
+        kc, vc = _dequant(u)
+        kn = K[b, h, T:].astype(np.float64)
+        if w.rope:
+            kn = np.stack([oracle.rope(kn[i], T + i, w.rope_base) for i in range(n)])
+        keys, vals = np.concatenate([kc, kn]), np.concatenate([vc, V[b, h, T:].astype(np.float64)])
+        step = 2.0 ** -11 * np.abs(keys) + 2.0 ** -19 * np.tile(np.hypot(keys[:, :64], keys[:, 64:]), 2)
+        for g in range(hg):
+            for i in range(n):
+                m, x = T + i + 1, q[b, h * hg + g, i].astype(np.float64)
+                s = keys[:m] @ x * w.softmax_scale
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                o = p @ vals[:m]
+                e = (step[:m] @ np.abs(x)).max() * w.softmax_scale
+                bound = np.expm1(2 * e) * (p @ np.abs(vals[:m] - o)) + 2.0 ** -10 * (p @ np.abs(vals[:m])) + 2.0 ** -11 * np.abs(o) + 1e-6
+                err = np.abs(out[b, h * hg + g, i] - o)
+                worst = max(worst, (err / bound).max())
+    print(f"worst {worst:.3f} of the bound")
+    assert worst <= 1.0
+    cache.close()
+
+
 @pytest.mark.parametrize("method,sink,pieces", [
     ("k2v2", 0, [1, 127, 1, 128, 257, 3, 130]),
     ("k2v2", 5, [3, 2, 128, 128, 1, 300]),
