@@ -34,7 +34,7 @@
 //
 // What bounds it (GB300; 1863 TFLOP/s bf16 and 6801 GB/s measured, 4 D flops per visible pair of query and key):
 //   A  512 tokens, batch 4 x 40 heads over 8192 tokens, K4V2      372 us   354 GFLOP: 950 TFLOP/s, 0.51
-//   B  a whole prompt of 4099 tokens, batch 2 x 32 heads on 8     343 us   275 GFLOP: 803 TFLOP/s, 0.43 (kvq_chunk_step)
+//   B  a whole prompt of 4099 tokens, batch 2 x 32 heads on 8     329 us   275 GFLOP: 836 TFLOP/s, 0.45 (kvq_chunk_step)
 //   C  8 tokens, batch 32 x 32 heads on 8 over 32768, K2V2        566 us   824 MB of pages: 1.46 TB/s, 0.21
 //   D  33 tokens, 32 heads on 8 over 1,048,576, K3V3, rotated     2.08 ms  567 GFLOP, 990 MB of pages
 // Long chunks (A, B): a tile of 256 rows x 128 keys takes 4,050 cycles, its products 2,740 at the matrix rate; the
@@ -48,7 +48,7 @@
 // A 980 -> 461, B 1255 -> 660, C 1366 -> 723; an issuing warp that waits once a step, A 461 -> 391, C 723 -> 616; a row
 // of codes in registers, a low tile of 16 columns and two producer sets for rotated keys, D 4531 -> 2365; S read once,
 // A 399 -> 384; zero points prepared once per block, C 655 -> 576; new tokens copied straight into place, B 528 -> 451;
-// start-up costs in the cuts, B 451 -> 343; sparse entries written over the dense keys and loops compiled per code
+// start-up costs in the cuts, B 451 -> 329; sparse entries written over the dense keys and loops compiled per code
 // width, D 2252 -> 2077.  Tried and slower: unrolled producer loops (instruction-cache misses), a 16-column
 // double-buffered softmax, 64 columns a pass with registers moved between warpgroups (spills), sixteen softmax warps,
 // both streams on both halves of the rows, two sets of key producers where keys are not rotated, bitstream zero points
@@ -76,9 +76,9 @@ constexpr int kThreads = (8 + (kKeySets<ROPE> + 1) * kProducers + 1) * 32;
 constexpr float kLazy = 8.0f;      // log2 units the running maximum may lag behind
 constexpr float kWeightExp = 7.0f; // weights are at most 2^(8 + 7): below fp16's 65504
 // A job costs more than its tiles: its queries are fetched, the pipeline fills, its rows are written.  The cuts between
-// CTAs count that as three tiles (measured: 13,000 cycles a job, 4,000 a tile); without it a CTA with the short jobs of a
-// prompt's beginning took half as long again as the others.
-constexpr int kJobCost = 3;
+// CTAs count that as four tiles (13,000 cycles a job, 3,000 to 4,000 a tile).  A prompt of 4099 tokens, whose first jobs
+// are short, takes 451 us without it, and 367, 344, 329, 336, 347, 363 with 2, 3, 4, 5, 7, 10; other workloads hardly move.
+constexpr int kJobCost = 4;
 constexpr int kTmemColumns = 512;  // S / P of the two streams at 0 and 128, O at 256 and 384
 constexpr int kValueStages = 2;
 constexpr int kBadSlots = 4;       // marks of non-finite values: producers run at most three jobs ahead
